@@ -77,6 +77,7 @@ typedef enum { SDK_F32 = 0, SDK_BF16 = 1 } sdk_dtype;
 #define SDK_K_ATOMS 16        /* atoms per stored code                     */
 #define SDK_KLOW_PLANES 3     /* words kept in the k_lo planes             */
 #define SDK_MAX_BATCH 64      /* sequences per decode / append call        */
+#define SDK_MAX_REQUESTS 4096 /* requests per call on the paged store      */
 #define SDK_WS_ALIGN 256      /* required alignment of workspaces (bytes)  */
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -401,6 +402,135 @@ typedef struct {
 SDK_API sdk_status sdk_decode_layout_of(int32_t B, int32_t Hq, int32_t head_dim,
                                 int32_t n_atoms, int64_t max_len,
                                 sdk_decode_layout* layout_out /* host */);
+
+/* ------------------------------------------------------------ paged store
+ * A pool of pages shared by many requests, for serving loops whose plans
+ * are made on the device.  One array
+ *   pages  uint32 [n_pages][Hkv][page_size][2][16]
+ * holds, per page and KV head, page_size token slots; a slot is the 16 key
+ * words and the 16 value words of a token (one 128-byte line).  Slot number
+ * s = page * page_size + offset; n_pages * page_size < 2^31; any page_size
+ * from 1 to 65536.  A request's tokens lie in the pages of its row of
+ *   block_table  int32 [B][max_pages]  page of tokens [c page_size,
+ *                (c + 1) page_size) in column c; entries behind a request's
+ *                last page are never read.
+ * Lengths are device arrays here (int32), so that a step can be planned,
+ * captured and replayed without the host; what the host passes are bounds.
+ * Conditions found on the device are recorded in the workspace header
+ * (sdk_check_status): SDK_ERR_CAPACITY where a bound or the pool does not
+ * suffice, SDK_ERR_DEVICE_CHECK for a page, slot, atom index or offset out
+ * of range.  The paper describes the per-token codes and the static
+ * dictionary (review, FAQ on the 15x compression), not their paging.
+ *
+ * sdk_block_tables -- the plan of one step.  For request b with L = lens[b]
+ * tokens in the cache and n = n_new[b] to come, its pages [ceil(L /
+ * page_size), ceil((L + n) / page_size)) are taken from the stack of free
+ * ones, in the order of the requests: the j-th page taken in all is
+ * free_pages[n_free - 1 - j].
+ *   lens, n_new  device, int32 [B], 1 <= B <= SDK_MAX_REQUESTS
+ *   free_pages   device, int32 [n_stack]: the first n_free[0] are free
+ *   n_free       device, int32 [1], 0 <= n_free[0] <= n_stack
+ *   block_table  device, int32 [B][max_pages]; the new entries are written,
+ *                all others stay
+ *   max_new      rows of slot_map, >= 1
+ *   slot_map     device, int64 [max_new], 8-byte aligned: the slot of every
+ *                new token, request after request; -1 for the tokens of a
+ *                refused request and for the rows behind the last one
+ *   cu_new       device, int32 [B + 1]: the first row of every request and
+ *                the number of rows (at most max_new)
+ *   new_lens     device, int32 [B]: L + n (L for a refused request)
+ *   n_free_out   device, int32 [1]: pages left
+ * A request is refused as a whole, and takes no page, when L + n needs more
+ * than max_pages columns, when its rows pass max_new, when the pages up to
+ * and including its own exceed n_free[0] (SDK_ERR_CAPACITY), or when L or n
+ * is negative or L + n passes 2^31 - 1 (SDK_ERR_DEVICE_CHECK).  The outputs
+ * must not overlap the inputs (SDK_ERR_INVALID_ARG): the call changes none
+ * of its inputs but the table, so repeating it gives the same plan.
+ */
+SDK_API size_t sdk_block_tables_workspace_bytes(int32_t B);
+SDK_API sdk_status sdk_block_tables(const int32_t* lens, const int32_t* n_new, int32_t B,
+                            const int32_t* free_pages, int32_t n_stack,
+                            const int32_t* n_free, int32_t n_pages, int32_t page_size,
+                            int32_t* block_table, int32_t max_pages,
+                            int64_t max_new, int64_t* slot_map, int32_t* cu_new,
+                            int32_t* new_lens, int32_t* n_free_out,
+                            void* workspace, size_t ws_bytes,
+                            sdk_stream_t stream);
+
+/* sdk_paged_store -- writes the code words of n_tok tokens to their slots.
+ *   codes_k, codes_v  device, uint32 [n_tok][Hkv][16], 16-byte aligned (the
+ *                words of sdk_encode over [n_tok][Hkv][head_dim])
+ *   slot_map     device, int64 [n_tok]; a negative slot is skipped; slots
+ *                of one call must differ (of a repeated slot's tokens it is
+ *                not specified whose words stay)
+ * A slot >= n_pages * page_size is skipped and recorded
+ * (SDK_ERR_DEVICE_CHECK).
+ * sdk_paged_append -- sdk_encode of xk and xv [n_tok][Hkv][head_dim] (fp32
+ * or bf16) over the two dictionaries, followed by sdk_paged_store. */
+SDK_API size_t sdk_paged_store_workspace_bytes(void);
+SDK_API sdk_status sdk_paged_store(const uint32_t* codes_k, const uint32_t* codes_v,
+                           int64_t n_tok, int32_t Hkv, const int64_t* slot_map,
+                           uint32_t* pages, int32_t n_pages, int32_t page_size,
+                           void* workspace, size_t ws_bytes, sdk_stream_t stream);
+SDK_API size_t sdk_paged_append_workspace_bytes(int64_t n_tok, int32_t Hkv,
+                                        int32_t head_dim, int32_t n_atoms);
+SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dtype,
+                            int64_t n_tok, int32_t Hkv, int32_t head_dim,
+                            const void* dict_k, const void* dict_v, int32_t n_atoms,
+                            const int64_t* slot_map, uint32_t* pages,
+                            int32_t n_pages, int32_t page_size, void* workspace,
+                            size_t ws_bytes, sdk_stream_t stream);
+
+#define SDK_CHUNK_CAUSAL 1    /* a token sees the tokens up to its own      */
+
+/* sdk_chunk_attn -- attention of the new tokens of every request over its
+ * paged codes: a whole prompt, a piece of one, a few drafted tokens or one
+ * generated token per request, mixed as they come.  Request b has
+ * len = lens[b] tokens in the store, the n = cu_q[b+1] - cu_q[b] new ones
+ * among them (append first); its row i stands at position p = len - n + i
+ * and sees the tokens t < len with, under SDK_CHUNK_CAUSAL, t <= p, and with
+ * window > 0 also t > p - window.  Every token takes part with all 16 atoms
+ * (no selection):
+ *   K_t = sum_j c_tj D_K[i_tj],  V_t = sum_j c_tj D_V[i_tj]
+ *   out_i = sum_t p_it V_t,  p_i = softmax over the seen t of
+ *           scale <q_i, K_t>
+ * A row that sees nothing (p < 0, or len = 0) gives out = 0, lse = -inf.
+ *   q          device, bf16 [n_tok][Hq][head_dim], 16-byte aligned
+ *   n_tok      rows of q, out and lse; rows from cu_q[B] on are not touched
+ *   cu_q       device, int32 [B + 1], rising from >= 0 to <= n_tok
+ *   lens       device, int32 [B]
+ *   max_q, max_len   host bounds on every n and every len (>= 1)
+ *   total_len  host bound on the sum of lens (0: B * max_len)
+ *   window     0 (none), or >= 1 with SDK_CHUNK_CAUSAL
+ *   flags      0 or SDK_CHUNK_CAUSAL
+ *   out        device, bf16 [n_tok][Hq][head_dim], 16-byte aligned
+ *   lse        device, float [n_tok][Hq], or NULL: log sum_t exp(scale
+ *              <q_i, K_t>), natural logarithm (to merge with attention over
+ *              other tokens)
+ *   workspace  device, >= sdk_chunk_attn_workspace_bytes() of the same sizes
+ * Limits: B <= SDK_MAX_REQUESTS, Hq % Hkv == 0, head_dim 64 or 128, scale >
+ *   0, n_tok * Hq < 2^31, max_pages * page_size >= max_len.
+ * Arithmetic: rebuilt vectors and probabilities enter the products in fp16
+ *   (fp32 sums); q exactly.  A rebuilt entry beyond +-65504 or NaN is
+ *   recorded (SDK_ERR_DEVICE_CHECK) and taken as +-65504 or 0; below 2^-14
+ *   it keeps an absolute error of 2^-25, as the coefficients themselves do.
+ * A request whose cu_q, n or len lies outside its bounds is refused:
+ *   recorded, its rows are not touched.
+ */
+SDK_API size_t sdk_chunk_attn_workspace_bytes(int32_t B, int64_t n_tok, int32_t Hq,
+                                      int32_t Hkv, int32_t head_dim,
+                                      int32_t n_atoms, int32_t max_q,
+                                      int32_t max_len, int64_t total_len);
+SDK_API sdk_status sdk_chunk_attn(const void* q, int64_t n_tok, int32_t B, int32_t Hq,
+                          int32_t Hkv, int32_t head_dim, const void* dict_k,
+                          const void* dict_v, int32_t n_atoms,
+                          const uint32_t* pages, int32_t n_pages,
+                          int32_t page_size, const int32_t* block_table,
+                          int32_t max_pages, const int32_t* lens,
+                          const int32_t* cu_q, int32_t max_q, int32_t max_len,
+                          int64_t total_len, int32_t window, int32_t flags,
+                          float scale, void* out, float* lse, void* workspace,
+                          size_t ws_bytes, sdk_stream_t stream);
 
 /* ------------------------------------------------------------ workspaces
  * Every workspace starts with a 256-byte header:

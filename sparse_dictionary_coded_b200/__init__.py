@@ -10,6 +10,7 @@ module only marshals torch tensors (device memory) and the current CUDA
 stream into the C ABI declared in include/sdk.h, under the same names.
 """
 
+import collections
 import ctypes
 import math
 
@@ -17,7 +18,7 @@ import torch
 
 from . import _capi
 from ._capi import (SDK_OK, SDK_F32, SDK_BF16, MAX_ATOMS, K_ATOMS,
-                    KLOW_PLANES, MAX_BATCH, SDK_DECODE_FULL_SOFTMAX,
+                    KLOW_PLANES, MAX_BATCH, SDK_CHUNK_CAUSAL, SDK_DECODE_FULL_SOFTMAX,
                     SDK_DECODE_INT_SOFTMAX, SDK_DECODE_KEEP_KEYS,
                     SDK_DECODE_SELECT_RADIX, SDK_DECODE_SELECT_BRACKET, DecodeLayout,
                     load)
@@ -29,7 +30,11 @@ __all__ = [
     "sdk_decode_layout_of", "sdk_workspace_init", "sdk_check_status",
     "new_workspace", "CodeStore", "read_select_state", "sdk_timing_enable",
     "sdk_set_exchange_timeout_ns", "decode_flags",
-    "sdk_timing_read",
+    "sdk_timing_read", "PagedCodeStore", "BlockTables", "sdk_block_tables",
+    "sdk_block_tables_workspace_bytes", "sdk_paged_store",
+    "sdk_paged_store_workspace_bytes", "sdk_paged_append",
+    "sdk_paged_append_workspace_bytes", "sdk_chunk_attn",
+    "sdk_chunk_attn_workspace_bytes",
 ]
 
 
@@ -296,3 +301,255 @@ def sdk_decode_attn(q, dict_k, dict_v, store, klow=3, khigh=16, top_num=1,
                              workspace.numel(), _stream(stream))
     _check(rc, "sdk_decode_attn")
     return out
+
+
+# ------------------------------------------------------------- paged store
+
+def _same_device(first, **others):
+    """Every tensor on the device of `first` (a kernel reads them all)."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError("%s is on %s, the other tensors on %s" %
+                             (name, t.device, first.device))
+    return first.device
+
+
+def _shape(t, name, *dims):
+    if tuple(t.shape) != dims:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), dims))
+    return t
+
+
+def _pages(pages):
+    pages = _cuda_contig(pages, "pages", (torch.int32,))
+    if pages.dim() != 5 or tuple(pages.shape[3:]) != (2, K_ATOMS):
+        raise ValueError("pages must be [n_pages, Hkv, page_size, 2, %d]" % K_ATOMS)
+    return pages
+
+
+BlockTables = collections.namedtuple(
+    "BlockTables", "block_table slot_map cu_new new_lens n_free")
+
+
+def sdk_block_tables_workspace_bytes(B):
+    return load().sdk_block_tables_workspace_bytes(B)
+
+
+def sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size,
+                     max_new, n_pages=None, slot_map=None, cu_new=None,
+                     new_lens=None, n_free_out=None, workspace=None,
+                     stream=None):
+    """The plan of one step, made on the device: pages for n_new more tokens
+    of every request, taken from the stack free_pages[:n_free] and entered
+    into block_table (in place), the slot of every new token, and the row
+    offsets and lengths that sdk_chunk_attn takes.  lens, n_new int32 [B],
+    free_pages int32 [n_pages], n_free int32 [1], block_table int32
+    [B, max_pages]; max_new: rows of the slot map (a bound on the step's
+    tokens).  n_pages: pages of the pool (default: the length of
+    free_pages, which may hold fewer entries than the pool has pages).
+    Returns BlockTables; requests that do not fit are refused and recorded
+    in the workspace (include/sdk.h)."""
+    lib = load()
+    lens = _cuda_contig(lens, "lens", (torch.int32,))
+    n_new = _cuda_contig(n_new, "n_new", (torch.int32,))
+    free_pages = _cuda_contig(free_pages, "free_pages", (torch.int32,))
+    n_free = _cuda_contig(n_free, "n_free", (torch.int32,))
+    table = _cuda_contig(block_table, "block_table", (torch.int32,))
+    if lens.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("lens and free_pages have one dimension, block_table two")
+    B = lens.shape[0]
+    _shape(n_new, "n_new", B)
+    _shape(n_free, "n_free", 1)
+    if table.shape[0] != B:
+        raise ValueError("block_table has %d rows for %d requests" % (table.shape[0], B))
+    if n_pages is None:
+        n_pages = free_pages.shape[0]
+    dev = lens.device
+
+    def made(t, name, dtype, n):
+        if t is None:
+            return torch.empty(n, dtype=dtype, device=dev)
+        return _shape(_cuda_contig(t, name, (dtype,)), name, n)
+
+    slot_map = made(slot_map, "slot_map", torch.int64, max_new)
+    cu_new = made(cu_new, "cu_new", torch.int32, B + 1)
+    new_lens = made(new_lens, "new_lens", torch.int32, B)
+    n_free_out = made(n_free_out, "n_free_out", torch.int32, 1)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = new_workspace(lib.sdk_block_tables_workspace_bytes(B), dev)
+        _same_device(lens, n_new=n_new, free_pages=free_pages, n_free=n_free,
+                     block_table=table, slot_map=slot_map, cu_new=cu_new,
+                     new_lens=new_lens, n_free_out=n_free_out, workspace=workspace)
+        rc = lib.sdk_block_tables(
+            _ptr(lens), _ptr(n_new), B, _ptr(free_pages), free_pages.shape[0], _ptr(n_free),
+            n_pages, page_size, _ptr(table), table.shape[1], max_new, _ptr(slot_map),
+            _ptr(cu_new), _ptr(new_lens), _ptr(n_free_out), _ptr(workspace),
+            workspace.numel(), _stream(stream))
+    _check(rc, "sdk_block_tables")
+    return BlockTables(table, slot_map, cu_new, new_lens, n_free_out)
+
+
+def sdk_paged_store_workspace_bytes():
+    return load().sdk_paged_store_workspace_bytes()
+
+
+def sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace=None,
+                    stream=None):
+    """Writes the code words codes_k, codes_v int32 [n_tok, Hkv, 16] (or
+    [n_tok * Hkv, 16], as sdk_encode returns them) to their slots of pages
+    int32 [n_pages, Hkv, page_size, 2, 16]; slot_map int64 [n_tok], negative
+    slots are skipped.  Returns pages."""
+    lib = load()
+    pages = _pages(pages)
+    n_pages, Hkv, page_size = pages.shape[:3]
+    slot_map = _cuda_contig(slot_map, "slot_map", (torch.int64,))
+    n_tok = slot_map.numel()
+    for t, name in ((codes_k, "codes_k"), (codes_v, "codes_v")):
+        _cuda_contig(t, name, (torch.int32,))
+        if t.shape[-1] != K_ATOMS or t.numel() != n_tok * Hkv * K_ATOMS:
+            raise ValueError("%s must hold %d words of %d heads for %d tokens" %
+                             (name, K_ATOMS, Hkv, n_tok))
+    with torch.cuda.device(pages.device):
+        if workspace is None:
+            workspace = new_workspace(lib.sdk_paged_store_workspace_bytes(), pages.device)
+        _same_device(pages, codes_k=codes_k, codes_v=codes_v, slot_map=slot_map,
+                     workspace=workspace)
+        rc = lib.sdk_paged_store(_ptr(codes_k), _ptr(codes_v), n_tok, Hkv, _ptr(slot_map),
+                                 _ptr(pages), n_pages, page_size, _ptr(workspace),
+                                 workspace.numel(), _stream(stream))
+    _check(rc, "sdk_paged_store")
+    return pages
+
+
+def sdk_paged_append_workspace_bytes(n_tok, Hkv, head_dim, n_atoms):
+    return load().sdk_paged_append_workspace_bytes(n_tok, Hkv, head_dim, n_atoms)
+
+
+def sdk_paged_append(pages, xk, xv, dict_k, dict_v, slot_map, workspace=None,
+                     stream=None):
+    """Encodes xk, xv [n_tok, Hkv, head_dim] (fp32 or bf16) and writes their
+    codes to the slots slot_map int64 [n_tok] of pages.  Returns the
+    workspace (its header records what the device found)."""
+    lib = load()
+    pages = _pages(pages)
+    n_pages, Hkv, page_size = pages.shape[:3]
+    xk = _cuda_contig(xk, "xk", (torch.float32, torch.bfloat16))
+    xv = _cuda_contig(xv, "xv", (xk.dtype,))
+    dk = _cuda_contig(dict_k, "dict_k", (torch.bfloat16,))
+    dv = _cuda_contig(dict_v, "dict_v", (torch.bfloat16,))
+    slot_map = _cuda_contig(slot_map, "slot_map", (torch.int64,))
+    n_tok = slot_map.numel()
+    n_atoms, d = dk.shape
+    _shape(dv, "dict_v", n_atoms, d)
+    _shape(xk, "xk", n_tok, Hkv, d)
+    _shape(xv, "xv", n_tok, Hkv, d)
+    with torch.cuda.device(pages.device):
+        if workspace is None:
+            workspace = new_workspace(
+                lib.sdk_paged_append_workspace_bytes(n_tok, Hkv, d, n_atoms), pages.device)
+        _same_device(pages, xk=xk, xv=xv, dict_k=dk, dict_v=dv, slot_map=slot_map,
+                     workspace=workspace)
+        rc = lib.sdk_paged_append(_ptr(xk), _ptr(xv), _x_dtype(xk), n_tok, Hkv, d, _ptr(dk),
+                                  _ptr(dv), n_atoms, _ptr(slot_map), _ptr(pages), n_pages,
+                                  page_size, _ptr(workspace), workspace.numel(),
+                                  _stream(stream))
+    _check(rc, "sdk_paged_append")
+    return workspace
+
+
+def sdk_chunk_attn_workspace_bytes(B, n_tok, Hq, Hkv, head_dim, n_atoms, max_q,
+                                   max_len, total_len=0):
+    return load().sdk_chunk_attn_workspace_bytes(B, n_tok, Hq, Hkv, head_dim, n_atoms, max_q,
+                                                 max_len, total_len)
+
+
+def sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q,
+                   max_len, total_len=0, causal=True, window=0, scale=None,
+                   out=None, lse=None, workspace=None, stream=None):
+    """Attention of every request's new tokens over its paged codes.  q bf16
+    [n_tok, Hq, head_dim], the requests' rows one after the other (row
+    offsets cu_q int32 [B + 1]); lens int32 [B]: tokens in the store, the new
+    ones among them; block_table int32 [B, max_pages].  max_q, max_len and
+    total_len are host bounds on the new tokens and the context of a request
+    and on all contexts together (0: B * max_len).  Returns out bf16 [n_tok,
+    Hq, head_dim]; lse: a float32 [n_tok, Hq] tensor that receives the
+    logarithms of the softmax sums."""
+    lib = load()
+    pages = _pages(pages)
+    n_pages, Hkv, page_size = pages.shape[:3]
+    q = _cuda_contig(q, "q", (torch.bfloat16,))
+    dk = _cuda_contig(dict_k, "dict_k", (torch.bfloat16,))
+    dv = _cuda_contig(dict_v, "dict_v", (torch.bfloat16,))
+    table = _cuda_contig(block_table, "block_table", (torch.int32,))
+    lens = _cuda_contig(lens, "lens", (torch.int32,))
+    cu_q = _cuda_contig(cu_q, "cu_q", (torch.int32,))
+    if q.dim() != 3 or lens.dim() != 1 or table.dim() != 2:
+        raise ValueError("q has three dimensions, lens one, block_table two")
+    n_tok, Hq, d = q.shape
+    n_atoms = dk.shape[0]
+    B = lens.shape[0]
+    _shape(dk, "dict_k", n_atoms, d)
+    _shape(dv, "dict_v", n_atoms, d)
+    _shape(cu_q, "cu_q", B + 1)
+    if table.shape[0] != B:
+        raise ValueError("block_table has %d rows for %d requests" % (table.shape[0], B))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shape(_cuda_contig(out, "out", (torch.bfloat16,)), "out", n_tok, Hq, d)
+    if lse is not None:
+        _shape(_cuda_contig(lse, "lse", (torch.float32,)), "lse", n_tok, Hq)
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            workspace = new_workspace(
+                lib.sdk_chunk_attn_workspace_bytes(B, n_tok, Hq, Hkv, d, n_atoms, max_q,
+                                                   max_len, total_len), q.device)
+        _same_device(q, dict_k=dk, dict_v=dv, pages=pages, block_table=table, lens=lens,
+                     cu_q=cu_q, out=out, lse=lse, workspace=workspace)
+        rc = lib.sdk_chunk_attn(
+            _ptr(q), n_tok, B, Hq, Hkv, d, _ptr(dk), _ptr(dv), n_atoms, _ptr(pages), n_pages,
+            page_size, _ptr(table), table.shape[1], _ptr(lens), _ptr(cu_q), max_q, max_len,
+            total_len, window, SDK_CHUNK_CAUSAL if causal else 0, float(scale), _ptr(out),
+            _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "sdk_chunk_attn")
+    return out
+
+
+class PagedCodeStore:
+    """The pool of one layer's code pages with its stack of free pages
+    (layout of include/sdk.h).  A serving loop plans a step, appends the new
+    tokens' vectors and attends, all from device lengths:
+
+        plan = store.plan(lens, n_new, block_table, max_new)
+        sdk_paged_append(store.pages, xk, xv, dict_k, dict_v, plan.slot_map)
+        out = sdk_chunk_attn(q, dict_k, dict_v, store.pages, block_table,
+                             plan.new_lens, plan.cu_new, max_q, max_len)
+    """
+
+    def __init__(self, n_pages, Hkv, page_size, device="cuda"):
+        self.n_pages, self.Hkv, self.page_size = n_pages, Hkv, page_size
+        self.pages = torch.zeros(n_pages, Hkv, page_size, 2, K_ATOMS, dtype=torch.int32,
+                                 device=device)
+        # page 0 on top of the stack
+        self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+
+    def plan(self, lens, n_new, block_table, max_new, workspace=None, stream=None):
+        """sdk_block_tables over this pool's free pages; the stack then holds
+        what is left (a new n_free tensor replaces the old one)."""
+        r = sdk_block_tables(lens, n_new, self.free_pages, self.n_free, block_table,
+                             self.page_size, max_new, n_pages=self.n_pages,
+                             workspace=workspace, stream=stream)
+        self.n_free = r.n_free
+        return r
+
+    def release(self, page_ids):
+        """Puts the pages of a finished request (int32 tensor of distinct
+        pages in use, none negative) back on the stack."""
+        n = page_ids.numel()
+        at = self.n_free.long() + torch.arange(n, device=self.free_pages.device)
+        self.free_pages[at] = page_ids.to(torch.int32)
+        self.n_free = self.n_free + n

@@ -19,6 +19,8 @@ STATUS_NAMES = {
 SDK_F32, SDK_BF16 = 0, 1
 SDK_DECODE_FULL_SOFTMAX, SDK_DECODE_INT_SOFTMAX, SDK_DECODE_KEEP_KEYS = 1, 2, 4
 SDK_DECODE_SELECT_RADIX, SDK_DECODE_SELECT_BRACKET = 8, 16
+SDK_CHUNK_CAUSAL = 1
+MAX_REQUESTS = 4096
 MAX_ATOMS, K_ATOMS, KLOW_PLANES, MAX_BATCH, WS_ALIGN = 32768, 16, 3, 64, 256
 DECODE_STATIC_WS_BYTES = 16 << 20
 
@@ -57,6 +59,23 @@ SIGNATURES = {
     "sdk_decode_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i64]),
     "sdk_decode_layout_of": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i64,
                                             _vp]),
+    "sdk_block_tables_workspace_bytes": (_sz, [_i32]),
+    "sdk_block_tables": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _vp, _i32,
+                                        _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp,
+                                        _vp, _sz, _vp]),
+    "sdk_paged_store_workspace_bytes": (_sz, []),
+    "sdk_paged_store": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, _i32,
+                                       _i32, _vp, _sz, _vp]),
+    "sdk_paged_append_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "sdk_paged_append": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp,
+                                        _vp, _i32, _vp, _vp, _i32, _i32, _vp,
+                                        _sz, _vp]),
+    "sdk_chunk_attn_workspace_bytes": (_sz, [_i32, _i64, _i32, _i32, _i32,
+                                             _i32, _i32, _i32, _i64]),
+    "sdk_chunk_attn": (ctypes.c_int, [_vp, _i64, _i32, _i32, _i32, _i32, _vp,
+                                      _vp, _i32, _vp, _i32, _i32, _vp, _i32,
+                                      _vp, _vp, _i32, _i32, _i64, _i32, _i32,
+                                      _f32, _vp, _vp, _vp, _sz, _vp]),
     "sdk_workspace_init": (ctypes.c_int, [_vp, _sz, _vp]),
     "sdk_check_status": (ctypes.c_int, [_vp, _vp, _vp]),
     "sdk_timing_enable": (ctypes.c_int, [_i32]),

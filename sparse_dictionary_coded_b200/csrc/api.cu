@@ -4,7 +4,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "sdk_internal.cuh"
+#include "paged.cuh"
 
 namespace sdk {
 
@@ -131,6 +131,20 @@ static sdk_status encode_core(bool allow_tc, const EncodeParams& p, int head_dim
     if (taken) return s;
   }
   return launch_encode_simt(p, head_dim, st);
+}
+
+// The key and value vectors of an append: one tensor-core launch over the
+// row tiles of both streams or, where it does not apply, one encode each.
+static sdk_status encode_both(const EncodeParams* pe, int head_dim, void* scratch,
+                              size_t scratch_bytes, cudaStream_t st) {
+  bool taken = false;
+  sdk_status rc = launch_encode_tc(pe, 2, head_dim, scratch, scratch_bytes, st, &taken);
+  if (rc != SDK_OK) return rc;
+  for (int s = 0; s < 2 && !taken; ++s) {
+    rc = encode_core(true, pe[s], head_dim, scratch, scratch_bytes, st);
+    if (rc != SDK_OK) return rc;
+  }
+  return SDK_OK;
 }
 
 static sdk_status encode_impl(bool allow_tc, const void* x, int32_t x_dtype, int64_t n_vec,
@@ -291,9 +305,7 @@ sdk_status sdk_append(const void* xk, const void* xv, int32_t x_dtype, int32_t B
       return rc;
     }
   }
-  // K and V: one tensor-core launch over the row tiles of both streams
-  // (or, where it does not apply, one encode per stream), then the words
-  // go into the store
+  // K and V are encoded, then the words go into the store
   EncodeParams pe[2];
   for (int s = 0; s < 2; ++s) {
     EncodeParams& p = pe[s];
@@ -307,13 +319,8 @@ sdk_status sdk_append(const void* xk, const void* xv, int32_t x_dtype, int32_t B
     p.rsq = nullptr;
     p.hdr = reinterpret_cast<WsHeader*>(ws);
   }
-  bool taken = false;
-  sdk_status rc = launch_encode_tc(pe, 2, head_dim, scratch, scratch_bytes, st, &taken);
+  const sdk_status rc = encode_both(pe, head_dim, scratch, scratch_bytes, st);
   if (rc != SDK_OK) return rc;
-  for (int s = 0; s < 2 && !taken; ++s) {
-    rc = encode_core(true, pe[s], head_dim, scratch, scratch_bytes, st);
-    if (rc != SDK_OK) return rc;
-  }
   for (int s = 0; s < 2; ++s) {
     ScatterParams sp;
     sp.codes = codes2[s];
@@ -330,6 +337,252 @@ sdk_status sdk_append(const void* xk, const void* xv, int32_t x_dtype, int32_t B
     if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
   }
   return SDK_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------- paged store
+
+namespace {
+
+// the bounds every call on the paged store shares
+bool bad_pool(const void* pages, int32_t n_pages, int32_t page_size) {
+  return pages == nullptr || !aligned(pages, 16) || n_pages < 1 || page_size < 1 ||
+         page_size > 65536 || (int64_t)n_pages * page_size > 0x7FFFFFFF;
+}
+
+// tokens of a context, and 128-token tiles of a chunk call's workspace
+constexpr int32_t kMaxContext = 1 << 30;
+constexpr int64_t kMaxTiles = 1 << 26;
+
+bool bad_workspace(const void* ws) { return ws == nullptr || !aligned(ws, SDK_WS_ALIGN); }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sdk_block_tables_workspace_bytes(int32_t B) { return B < 1 ? 0 : sizeof(WsHeader); }
+
+sdk_status sdk_block_tables(const int32_t* lens, const int32_t* n_new, int32_t B,
+                            const int32_t* free_pages, int32_t n_stack, const int32_t* n_free,
+                            int32_t n_pages, int32_t page_size, int32_t* block_table, int32_t max_pages,
+                            int64_t max_new, int64_t* slot_map, int32_t* cu_new,
+                            int32_t* new_lens, int32_t* n_free_out, void* workspace,
+                            size_t ws_bytes, sdk_stream_t stream) {
+  if (B < 1 || B > SDK_MAX_REQUESTS || max_pages < 1 || max_new < 1 || max_new > 0x7FFFFFFF)
+    return SDK_ERR_INVALID_ARG;
+  if (n_stack < 1 || n_pages < 1 || page_size < 1 || page_size > 65536 ||
+      (int64_t)n_pages * page_size > 0x7FFFFFFF)
+    return SDK_ERR_INVALID_ARG;
+  if (!lens || !n_new || !free_pages || !n_free || !block_table || !slot_map || !cu_new ||
+      !new_lens || !n_free_out || bad_workspace(workspace))
+    return SDK_ERR_INVALID_ARG;
+  if (!aligned(lens, 4) || !aligned(n_new, 4) || !aligned(free_pages, 4) || !aligned(n_free, 4) ||
+      !aligned(block_table, 4) || !aligned(slot_map, 8) || !aligned(cu_new, 4) ||
+      !aligned(new_lens, 4) || !aligned(n_free_out, 4))
+    return SDK_ERR_INVALID_ARG;
+  const struct { const void* p; size_t n; } in[] = {
+      {lens, (size_t)B * 4}, {n_new, (size_t)B * 4}, {free_pages, (size_t)n_stack * 4}, {n_free, 4}},
+      out[] = {{block_table, (size_t)B * max_pages * 4}, {slot_map, (size_t)max_new * 8},
+               {cu_new, ((size_t)B + 1) * 4}, {new_lens, (size_t)B * 4}, {n_free_out, 4}};
+  for (int o = 0; o < 5; ++o) {
+    for (const auto& i : in)
+      if (overlap(i.p, i.n, out[o].p, out[o].n)) return SDK_ERR_INVALID_ARG;
+    for (int k = 0; k < o; ++k)
+      if (overlap(out[k].p, out[k].n, out[o].p, out[o].n)) return SDK_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < sizeof(WsHeader)) return SDK_ERR_CAPACITY;
+  TableParams p;
+  p.lens = lens;
+  p.n_new = n_new;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.table = block_table;
+  p.slot_map = slot_map;
+  p.cu_new = cu_new;
+  p.new_lens = new_lens;
+  p.n_free_out = n_free_out;
+  p.hdr = reinterpret_cast<WsHeader*>(workspace);
+  p.max_new = max_new;
+  p.B = B;
+  p.n_stack = n_stack;
+  p.n_pages = n_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  return launch_block_tables(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t sdk_paged_store_workspace_bytes(void) { return sizeof(WsHeader); }
+
+sdk_status sdk_paged_store(const uint32_t* codes_k, const uint32_t* codes_v, int64_t n_tok,
+                           int32_t Hkv, const int64_t* slot_map, uint32_t* pages,
+                           int32_t n_pages, int32_t page_size, void* workspace, size_t ws_bytes,
+                           sdk_stream_t stream) {
+  if (n_tok < 0 || n_tok > 0x7FFFFFFF || Hkv < 1 || Hkv > 65535 ||
+      bad_pool(pages, n_pages, page_size) || bad_workspace(workspace))
+    return SDK_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(WsHeader)) return SDK_ERR_CAPACITY;
+  if (n_tok == 0) return SDK_OK;
+  if (!codes_k || !codes_v || !slot_map || !aligned(codes_k, 16) || !aligned(codes_v, 16) ||
+      !aligned(slot_map, 8))
+    return SDK_ERR_INVALID_ARG;
+  StoreParams p;
+  p.codes_k = codes_k;
+  p.codes_v = codes_v;
+  p.slot_map = slot_map;
+  p.pages = pages;
+  p.hdr = reinterpret_cast<WsHeader*>(workspace);
+  p.n_tok = n_tok;
+  p.Hkv = Hkv;
+  p.n_pages = n_pages;
+  p.page_size = page_size;
+  return launch_paged_store(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// as sdk_append of one sequence: header, K and V codes, encoder scratch
+size_t sdk_paged_append_workspace_bytes(int64_t n_tok, int32_t Hkv, int32_t head_dim,
+                                        int32_t n_atoms) {
+  if (n_tok < 0 || n_tok > 0x7FFFFFFF) return 0;
+  return sdk_append_workspace_bytes(1, Hkv, (int32_t)n_tok, head_dim, n_atoms);
+}
+
+sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dtype, int64_t n_tok,
+                            int32_t Hkv, int32_t head_dim, const void* dict_k, const void* dict_v,
+                            int32_t n_atoms, const int64_t* slot_map, uint32_t* pages,
+                            int32_t n_pages, int32_t page_size, void* workspace, size_t ws_bytes,
+                            sdk_stream_t stream) {
+  if (n_tok < 0 || n_tok > 0x7FFFFFFF || Hkv < 1 || Hkv > 65535 ||
+      bad_pool(pages, n_pages, page_size) || bad_workspace(workspace))
+    return SDK_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return SDK_ERR_UNSUPPORTED;
+  if ((x_dtype != SDK_F32 && x_dtype != SDK_BF16) || n_atoms < 1 || n_atoms > SDK_MAX_ATOMS)
+    return SDK_ERR_INVALID_ARG;
+  if (n_tok == 0) return ws_bytes < sizeof(WsHeader) ? SDK_ERR_CAPACITY : SDK_OK;
+  const size_t xa = x_dtype == SDK_F32 ? 4 : 2;
+  if (!xk || !xv || !dict_k || !dict_v || !slot_map || !aligned(xk, xa) || !aligned(xv, xa) ||
+      !aligned(dict_k, 16) || !aligned(dict_v, 16) || !aligned(slot_map, 8))
+    return SDK_ERR_INVALID_ARG;
+  const size_t need = sdk_paged_append_workspace_bytes(n_tok, Hkv, head_dim, n_atoms);
+  if (ws_bytes < need) return SDK_ERR_CAPACITY;
+  const int64_t nv = n_tok * Hkv;
+  char* ws = reinterpret_cast<char*>(workspace);
+  const size_t hb = align_up(sizeof(WsHeader), 256);
+  const size_t cb = align_up((size_t)nv * kAtoms * 4, 256);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  SmallEncode e;
+  memset(&e, 0, sizeof(e));
+  for (int s = 0; s < 2; ++s) {
+    EncodeParams& p = e.p[s];
+    p.x = s == 0 ? xk : xv;
+    p.x_dtype = x_dtype;
+    p.n_vec = nv;
+    p.dict = reinterpret_cast<const uint16_t*>(s == 0 ? dict_k : dict_v);
+    p.n = n_atoms;
+    p.k_atoms = kAtoms;
+    p.codes = reinterpret_cast<uint32_t*>(ws + hb + s * cb);
+    p.rsq = nullptr;
+    p.hdr = reinterpret_cast<WsHeader*>(ws);
+  }
+  e.streams = 2;
+  e.head_dim = head_dim;
+  bool taken = false;
+  if (nv <= kSmallEncodeRows) {   // a few vectors: both streams in one atom-parallel launch
+    const sdk_status rc =
+        launch_encode_small(e, ws + hb + 2 * cb, need - hb - 2 * cb, st, &taken);
+    if (taken && rc != SDK_OK) return rc;
+  }
+  if (!taken) {
+    const sdk_status rc =
+        nv <= kSmallEncodeRows
+            ? encode_core(true, e.p[0], head_dim, ws + hb + 2 * cb, need - hb - 2 * cb, st)
+            : encode_both(e.p, head_dim, ws + hb + 2 * cb, need - hb - 2 * cb, st);
+    if (rc != SDK_OK) return rc;
+    if (nv <= kSmallEncodeRows) {
+      const sdk_status rv =
+          encode_core(true, e.p[1], head_dim, ws + hb + 2 * cb, need - hb - 2 * cb, st);
+      if (rv != SDK_OK) return rv;
+    }
+  }
+  return sdk_paged_store(e.p[0].codes, e.p[1].codes, n_tok, Hkv, slot_map, pages, n_pages,
+                         page_size, workspace, ws_bytes, stream);
+}
+
+size_t sdk_chunk_attn_workspace_bytes(int32_t B, int64_t n_tok, int32_t Hq, int32_t Hkv,
+                                      int32_t head_dim, int32_t n_atoms, int32_t max_q,
+                                      int32_t max_len, int64_t total_len) {
+  if (B < 1 || B > SDK_MAX_REQUESTS || n_tok < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
+      (head_dim != 64 && head_dim != 128) || n_atoms < 1 || max_q < 1 || max_len < 1 ||
+      max_len > kMaxContext || total_len < 0 || n_tok * Hq > 0x7FFFFFFF ||
+      chunk_cap_tiles(B, max_len, total_len) > kMaxTiles)
+    return 0;
+  return chunk_workspace_bytes(B, n_tok, Hq, Hkv, head_dim, n_atoms, max_q, max_len, total_len);
+}
+
+sdk_status sdk_chunk_attn(const void* q, int64_t n_tok, int32_t B, int32_t Hq, int32_t Hkv,
+                          int32_t head_dim, const void* dict_k, const void* dict_v,
+                          int32_t n_atoms, const uint32_t* pages, int32_t n_pages,
+                          int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                          const int32_t* lens, const int32_t* cu_q, int32_t max_q,
+                          int32_t max_len, int64_t total_len, int32_t window, int32_t flags,
+                          float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
+                          sdk_stream_t stream) {
+  if (B < 1 || B > SDK_MAX_REQUESTS || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 ||
+      n_tok < 0 || n_tok > 0x7FFFFFFF || n_tok * Hq > 0x7FFFFFFF)
+    return SDK_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return SDK_ERR_UNSUPPORTED;
+  if (n_atoms < 1 || n_atoms > SDK_MAX_ATOMS || max_q < 1 || max_len < 1 ||
+      max_len > kMaxContext || max_pages < 1 || total_len < 0 ||
+      chunk_cap_tiles(B, max_len, total_len) > kMaxTiles || window < 0 || (flags & ~SDK_CHUNK_CAUSAL) != 0 ||
+      (window > 0 && !(flags & SDK_CHUNK_CAUSAL)))
+    return SDK_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return SDK_ERR_INVALID_ARG;
+  if (bad_pool(pages, n_pages, page_size) || bad_workspace(workspace) ||
+      (int64_t)max_pages * page_size < max_len)
+    return SDK_ERR_INVALID_ARG;
+  if (!dict_k || !dict_v || !block_table || !lens || !cu_q || !aligned(dict_k, 16) ||
+      !aligned(dict_v, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(cu_q, 4))
+    return SDK_ERR_INVALID_ARG;
+  if (n_tok > 0 && (!q || !out || !aligned(q, 16) || !aligned(out, 16) ||
+                    (lse != nullptr && !aligned(lse, 4))))
+    return SDK_ERR_INVALID_ARG;
+  const size_t need = chunk_workspace_bytes(B, n_tok, Hq, Hkv, head_dim, n_atoms, max_q, max_len,
+                                            total_len);
+  if (ws_bytes < need) return SDK_ERR_CAPACITY;
+  if (n_tok == 0) return SDK_OK;
+  ChunkParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = reinterpret_cast<const uint16_t*>(q);
+  p.dk = reinterpret_cast<const uint16_t*>(dict_k);
+  p.dv = reinterpret_cast<const uint16_t*>(dict_v);
+  p.pages = pages;
+  p.table = block_table;
+  p.lens = lens;
+  p.cu_q = cu_q;
+  p.out = reinterpret_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.n_tok = n_tok;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.d = head_dim;
+  p.n = n_atoms;
+  p.n_pages = n_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.max_q = (int64_t)max_q > n_tok ? (int)n_tok : max_q;
+  p.max_len = max_len;
+  p.window = window >= max_len ? 0 : window;   // a window over all there can be
+  p.causal = (flags & SDK_CHUNK_CAUSAL) ? 1 : 0;
+  p.cap_tiles = (int)chunk_cap_tiles(B, max_len, total_len);
+  p.scale = scale;
+  return launch_chunk_attn(p, reinterpret_cast<char*>(workspace),
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
