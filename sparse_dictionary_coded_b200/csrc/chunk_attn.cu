@@ -5,6 +5,7 @@
 // once per call as fp16 tiles of 128 tokens in the workspace, and
 // chunk_attn_kernel computes softmax(scale q K^T) V over the tiles.
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace sdk {
 
@@ -17,16 +18,19 @@ constexpr int kRebTok = 32;       // tokens of one work item of rebuild_kernel
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct ChunkLayout {
-  size_t plan, kt, vt, total;
+  size_t plan, kt, vt, ml, po, total;
 };
 
-ChunkLayout chunk_layout(int B, int Hkv, int d, int64_t cap_tiles) {
+ChunkLayout chunk_layout(int B, int64_t rows, int Hkv, int d, int64_t cap_tiles, int splits) {
   ChunkLayout l;
   const size_t tiles = (size_t)cap_tiles * Hkv * kTile * d * 2;
   l.plan = sizeof(WsHeader);
   l.kt = up256(l.plan + (size_t)B * sizeof(ReqPlan));
   l.vt = l.kt + tiles;
-  l.total = l.vt + tiles;
+  l.ml = l.vt + tiles;
+  const size_t parts = splits > 1 ? (size_t)splits * rows : 0;
+  l.po = up256(l.ml + parts * 8);
+  l.total = up256(l.po + parts * d * 4);
   return l;
 }
 
@@ -191,49 +195,488 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
   }
 }
 
-// One warp per (row, query head): lanes hold D / 32 dims, one pass over the
-// tokens with the running maximum and sum.
+// ---------------------------------------------------------------- attention
+//
+// softmax(scale q K^T) V on the 5th-generation tensor cores.  The rows of a
+// KV head's query group are packed (row = token * g + head of the group),
+// a CTA takes 256 of them as two MMA tiles of 128 and walks the context's
+// rebuilt tiles once with the running maximum and sum:
+//   S = Q K^T         tcgen05, both operands from shared memory, fp32 in TMEM
+//   P = 2^(S c - m)   one row per thread; written back over S as fp16
+//   O = O + P V       tcgen05, P from TMEM, V as the MN-major operand
+// While the threads of one tile are in their exponentials, the tensor cores
+// work on the other's products.  Warps 0-3 and 4-7 hold the rows of the two
+// tiles, warp 8 issues the MMAs, warp 9 the copies (a tile image is
+// contiguous: one bulk copy each, into a ring).
+// The maximum m is only raised when a tile exceeds it by 2^8 (O then is
+// rescaled in TMEM, which is rare); P is 2^7 above its nominal range, so it
+// stays below 2^15 and its smallest fp16 step is 2^-31 of the row's largest
+// term: what 2^18 tokens lose by it is below 2^-13.
+// q enters as fp16 scaled by a power of two per row (exact: 8 significand
+// bits, the row's largest entry near 2^15).
+// A context may be split over several CTAs (few rows, long contexts); their
+// partial sums are joined by chunk_join_kernel.
+namespace {
+
+constexpr int kAThreads = 384;     // two warpgroups of rows, one of MMA and copy warps
+// registers a thread after the split: 256 x 224 + 128 x 56 = 384 x 168, what
+// the block is launched with (the rows' 128 scores stay in registers)
+constexpr int kRegsLaunch = 168, kRegsRows = 224, kRegsRest = 56;
+static_assert(256 * kRegsRows + 128 * kRegsRest == kAThreads * kRegsLaunch, "register split");
+constexpr float kPUp = 7.0f;       // log2 of P's offset
+constexpr float kSlack = 8.0f;     // log2 of how far a tile may exceed m
+
 template <int D>
-__global__ void __launch_bounds__(128) chunk_attn_kernel(ChunkParams p) {
+struct ACfg {
+  static constexpr int kTileB = kTile * D * 2;             // one Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kOffQ = kStages * kTileB;
+  static constexpr int kOffBar = kOffQ + 2 * kTileB;
+  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2;
+  static constexpr int kSmem = kOffBar + kNumBars * 8 + 64 + 1024;   // + alignment slack
+  static_assert(kSmem <= 232448, "exceeds the 227 KB shared memory of one sm_100 CTA");
+  // D f32, A and B f16; S: both K-major, N = 128; O: B MN-major, N = D
+  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) |
+                                      ((uint32_t)(kTile >> 4) << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                      ((uint32_t)(kTile >> 4) << 24);
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  const uint32_t z = 0u;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(z), "r"(z), "r"(z), "r"(z)
+      : "memory");
+}
+
+// 32 lanes x 32 bits, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p) {
+  using C = ACfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const int g = p.g;
+  // the work item: consecutive CTAs share a KV head's tiles
+  int w = blockIdx.x;
+  const int split = w % p.splits;
+  w /= p.splits;
+  const int mb = p.mblocks - 1 - w % p.mblocks;   // the longest rows of a causal call first
+  w /= p.mblocks;
+  const int h = w % p.Hkv, b = w / p.Hkv;
+  const ReqPlan rp = p.plan[b];
+  const int rows = rp.n * g;                       // packed rows of this KV head
+  const int r_base = mb * 2 * kTile;
+  if (r_base >= rows) return;
+  const int nact = rows - r_base > kTile ? 2 : 1;  // MMA tiles with rows
+
+  uint8_t* smem = tc::align_smem_1k(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffBar + C::kNumBars * 8);
+  volatile uint32_t* s_abort = misc + 0;
+  volatile uint32_t* s_tmem = misc + 1;
+  const uint32_t s0 = tc::smem_u32(smem);
+  auto bar_full = [&](int s) { return tc::smem_u32(&bars[s]); };
+  auto bar_empty = [&](int s) { return tc::smem_u32(&bars[C::kStages + s]); };
+  auto bar_s = [&](int i) { return tc::smem_u32(&bars[2 * C::kStages + i]); };
+  auto bar_p = [&](int i) { return tc::smem_u32(&bars[2 * C::kStages + 2 + i]); };
+  const uint32_t bar_q = tc::smem_u32(&bars[2 * C::kStages + 4]);
+  const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages + 5]);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // tiles the block's rows see, and this split's share of them
+  const int first_pos = rp.len - rp.n + r_base / g;
+  const int last_row = min(r_base + 2 * kTile, rows) - 1;
+  const int last_pos = rp.len - rp.n + last_row / g;
+  const int t_hi = p.causal ? min(last_pos + 1, rp.len) : rp.len;
+  const int t_lo = p.window > 0 ? max(0, first_pos - p.window + 1) : 0;
+  int ta = 0, tb = 0;
+  if (t_hi > t_lo) {
+    const int a0 = (t_lo - rp.lo) / kTile, nt = (t_hi - rp.lo + kTile - 1) / kTile - a0;
+    ta = a0 + (int)((int64_t)nt * split / p.splits);
+    tb = a0 + (int)((int64_t)nt * (split + 1) / p.splits);
+  }
+  const int nt = tb - ta;
+
+  if (tid == 0) {
+    *s_abort = 0u;
+    for (int s = 0; s < 2 * C::kStages + 2; ++s) tc::mbar_init(tc::smem_u32(&bars[s]), 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(bar_p(i), 4);
+    tc::mbar_init(bar_q, 4 * nact);
+    tc::mbar_init(bar_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32((const void*)s_tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  auto tm_s = [&](int i) { return tmem + (uint32_t)(i * kTile); };          // S, and P over it
+  auto tm_o = [&](int i) { return tmem + (uint32_t)(2 * kTile + i * D); };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 9 && lane == 0 && nt > 0) {
+    // ------------------------------------------------------------- copies
+      const char* kt = reinterpret_cast<const char*>(p.kt);
+      const char* vt = reinterpret_cast<const char*>(p.vt);
+      bool ok = true;
+      int issued = 0;
+      for (int k = 0; k < 2 * nt; ++k) {
+        const int st = k % C::kStages;
+        if (!tc::mbar_wait(bar_empty(st), ((uint32_t)(k / C::kStages) & 1u) ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        const int64_t tile = (int64_t)(rp.tile0 + ta + (k >> 1)) * p.Hkv + h;
+        tc::mbar_expect_tx(bar_full(st), (uint32_t)C::kTileB);
+        bulk_load(s0 + st * C::kTileB, ((k & 1) ? vt : kt) + tile * C::kTileB, (uint32_t)C::kTileB,
+                  bar_full(st));
+        issued = k + 1;
+      }
+      if (!ok) {
+        if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x78000000u | (blockIdx.x & 0xFFFFFFu));
+        *s_abort = 1u;
+      }
+      // every copy issued has landed before the CTA may leave
+      for (int k = max(0, issued - C::kStages); k < issued; ++k) {
+        uint32_t never = 0u;
+        tc::mbar_wait(bar_full(k % C::kStages), (uint32_t)(k / C::kStages) & 1u, &never, 100000000ull);
+      }
+    }
+    if (warp == 8 && lane == 0 && nt > 0) {
+    // --------------------------------------------------------------- MMAs
+      bool ok = tc::mbar_wait(bar_q, 0u, s_abort);
+      auto wait_full = [&](int k) {
+        return tc::mbar_wait(bar_full(k % C::kStages), (uint32_t)(k / C::kStages) & 1u, s_abort);
+      };
+      auto mma_s = [&](int i, int k) {
+        const uint32_t a = s0 + C::kOffQ + i * C::kTileB, bb = s0 + (k % C::kStages) * C::kTileB;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t o = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;
+          tc::tc_mma(tm_s(i), tc::smem_desc(a + o), tc::smem_desc(bb + o), C::kIdescS, ks > 0);
+        }
+        tc::tc_commit(bar_s(i));
+      };
+      if (ok) ok = wait_full(0);
+      if (ok) {
+        tc::tc_fence_after();
+        for (int i = 0; i < nact; ++i) mma_s(i, 0);
+        tc::tc_commit(bar_empty(0));
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+        const int kv = 2 * j + 1, kk = 2 * j + 2;
+        ok = wait_full(kv) && (j + 1 == nt || wait_full(kk));
+        for (int i = 0; ok && i < nact; ++i) {
+          ok = tc::mbar_wait(bar_p(i), (uint32_t)j & 1u, s_abort);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t vb = s0 + (kv % C::kStages) * C::kTileB;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_ts(tm_o(i), tm_s(i) + ks * 8, tc::smem_desc_mn(vb + ks * 2048, kTile * 128, 1024u),
+                   C::kIdescO, j > 0 || ks > 0);
+          if (j + 1 < nt)
+            mma_s(i, kk);
+          else
+            tc::tc_commit(bar_s(i));   // O complete
+        }
+        if (!ok) break;
+        tc::tc_commit(bar_empty(kv % C::kStages));
+        if (j + 1 < nt) tc::tc_commit(bar_empty(kk % C::kStages));
+      }
+      if (!ok) {
+        if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x79000000u | (blockIdx.x & 0xFFFFFFu));
+        *s_abort = 1u;
+        // what was issued ends before TMEM is freed
+        tc::tc_commit(bar_done);
+        uint32_t never = 0u;
+        tc::mbar_wait(bar_done, 0u, &never, 100000000ull);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+    if ((warp >> 2) < nact) {
+    // ------------------------------------------------------------ softmax
+    const int i = warp >> 2;
+    const int rr = (warp & 3) * 32 + lane;         // row of the MMA tile, TMEM lane
+    const int r = r_base + i * kTile + rr;         // packed row
+    const bool live = r < rows;
+    const int tok = live ? r / g : 0, hq = h * g + (live ? r - tok * g : 0);
+    const int64_t row = (int64_t)(rp.row0 + tok) * p.Hq + hq;
+    float c;                                       // S c = log2 of the softmax term
+    {
+      uint4 v[D / 8];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) v[k] = live ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t mx = 0u;                            // largest |q| as bf16 bits
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx = max(mx, max(x[u] & 0x7FFFu, (x[u] >> 16) & 0x7FFFu));
+      }
+      // 2^e q: the largest entry's exponent becomes 14 (e = 0 for a row of
+      // zeros or one with infinities or NaN, which spoil that row alone)
+      int e = (mx >> 7) == 0u || (mx >> 7) == 255u ? 0 : 14 + 127 - (int)(mx >> 7);
+      if (mx != 0u && (mx >> 7) == 0u) e = 126;    // subnormal: as far as one factor goes
+      const float up = __uint_as_float((uint32_t)(min(e, 126) + 127) << 23);
+      const float up2 = __uint_as_float((uint32_t)(max(e - 126, 0) + 127) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __half2 hh = __floats2half2_rn(bf16_lo(x[u]) * up * up2, bf16_hi(x[u]) * up * up2);
+          y[u] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        *reinterpret_cast<uint4*>(smem + C::kOffQ + i * C::kTileB + tile_off(rr, k)) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      c = p.scale * 1.44269504f / up / up2;
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_q);
+    }
+    const int pos = rp.len - rp.n + (live ? tok : last_row / g);
+    const int see1 = p.causal ? min(pos, rp.len - 1) : rp.len - 1;     // last token seen
+    const int see0 = p.window > 0 ? pos - p.window + 1 : 0;            // first one
+    // tiles that lie within every row's sight need no mask
+    const int w_hi = __reduce_min_sync(0xffffffffu, see1), w_lo = __reduce_max_sync(0xffffffffu, see0);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < nt; ++j) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), (uint32_t)j & 1u, s_abort));
+      if (!ok) break;
+      tc::tc_fence_after();
+      const int t0 = rp.lo + (ta + j) * kTile;
+      uint32_t v[4][32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tc::tmem_ld32(tm_s(i) + lanes + k * 32, v[k]);
+      tc::tmem_ld_wait();
+      if (t0 + kTile - 1 > w_hi || t0 < w_lo) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const int t = t0 + k * 32 + u;
+            if (t > see1 || t < see0) v[k][u] = 0xFF800000u;   // -inf
+          }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int u = 0; u < 32; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[k][u]));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      if (__any_sync(0xffffffffu, mt > m + kSlack)) {
+        // lane by lane, so that a row's result does not hang on its neighbours'
+        const float mn = mt > m + kSlack ? mt : m;
+        const float f = m == mn ? 1.0f : ex2(m - mn);
+        if (j > 0) {
+          l *= f;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            tc::tmem_ld32(tm_o(i) + lanes + k * 32, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+            tmem_st32(tm_o(i) + lanes + k * 32, o);
+          }
+        }
+        m = mn;
+      }
+      const float base = m == -INFINITY ? 0.0f : kPUp - m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t q2[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int e = 64 * k + 2 * u;
+          const float x0 = ex2(fmaf(__uint_as_float(v[e >> 5][e & 31]), c, base));
+          const float x1 = ex2(fmaf(__uint_as_float(v[e >> 5][(e & 31) + 1]), c, base));
+          sum[u & 1] += x0;
+          sum[2 + (u & 1)] += x1;
+          const __half2 hh = __floats2half2_rn(x0, x1);
+          q2[u] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        tmem_st32(tm_s(i) + lanes + k * 32, q2);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_p(i));
+    }
+    if (nt > 0 && ok) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), (uint32_t)nt & 1u, s_abort));
+      tc::tc_fence_after();
+    }
+    if (!ok && lane == 0) {
+      if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x7A000000u | (blockIdx.x & 0xFFFFFFu));
+      *s_abort = 1u;
+    }
+    // m carries P's offset from here on: O and l are sums of 2^(x - m)
+    const float mo = m == -INFINITY ? -INFINITY : m - kPUp;
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    if (p.splits == 1 && p.lse != nullptr && live && ok)
+      p.lse[row] = l > 0.0f || l != l ? (mo + log2f(l)) * 0.69314718f : -INFINITY;
+    if (p.splits > 1 && live && ok) {
+      p.part_ml[(int64_t)split * p.n_tok * p.Hq + row] = make_float2(mo, l);
+    }
+#pragma unroll 1
+    for (int k = 0; k < D / 32; ++k) {
+      uint32_t o[32];
+      if (nt > 0 && ok) {
+        tc::tmem_ld32(tm_o(i) + lanes + k * 32, o);
+        tc::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int u = 0; u < 32; ++u) o[u] = 0u;
+      }
+      if (live && ok) {
+        if (p.splits == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + k * 32);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 bb =
+                  __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                        __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+              y[e] = *reinterpret_cast<const uint32_t*>(&bb);
+            }
+            dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(
+              p.part_o + ((int64_t)split * p.n_tok * p.Hq + row) * D + k * 32);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        }
+      }
+    }
+    tc::tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// Joins the splits' partial sums, one warp per (row, query head).
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
   constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const ReqPlan rp = p.plan[blockIdx.y];
-  const int64_t e = (int64_t)blockIdx.x * 4 + warp;
-  const int i = (int)(e / p.Hq), hq = (int)(e % p.Hq);
-  if (i >= rp.n) return;
-  const int h = hq / p.g;
-  const int64_t row = (int64_t)(rp.row0 + i) * p.Hq + hq;
-  float q[E], o[E];
-#pragma unroll
-  for (int k = 0; k < E; ++k) {
-    q[k] = __uint_as_float((uint32_t)p.q[row * D + lane * E + k] << 16);
-    o[k] = 0.0f;
+  const int64_t R = p.n_tok * p.Hq;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  // rows of no request, or of a refused one, stay as they were
+  const int tok = (int)(row / p.Hq);
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_q[mid] <= tok) lo = mid; else hi = mid;
   }
-  const int pos = rp.len - rp.n + i;
-  const int t1 = p.causal ? min(pos + 1, rp.len) : rp.len;
-  const int t0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  float m = -INFINITY, z = 0.0f;
-  for (int t = t0; t < t1; ++t) {
-    const int tl = (t - rp.lo) / kTile, r = (t - rp.lo) % kTile;
-    const int64_t base = ((int64_t)(rp.tile0 + tl) * p.Hkv + h) * (kTile * D * 2);
-    const int off = tile_off(r, lane * E / 8) + (lane * E % 8) * 2;
-    const __half* kp = reinterpret_cast<const __half*>(reinterpret_cast<const char*>(p.kt) + base + off);
-    const __half* vp = reinterpret_cast<const __half*>(reinterpret_cast<const char*>(p.vt) + base + off);
-    float s = 0.0f;
+  const ReqPlan rp = p.plan[lo];
+  if (row >= R || tok < rp.row0 || tok >= rp.row0 + rp.n) return;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[s * R + row].x);
+  float z = 0.0f, o[E];
 #pragma unroll
-    for (int k = 0; k < E; ++k) s = fmaf(q[k], __half2float(kp[k]), s);
-    s = warp_sum(s) * p.scale;
-    const float mn = fmaxf(m, s), a = __expf(m - mn), x = __expf(s - mn);
-    z = z * a + x;
+  for (int k = 0; k < E; ++k) o[k] = 0.0f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[s * R + row];
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // saw nothing
+    const float f = ex2(ml.x - m);
+    z = fmaf(ml.y, f, z);
+    const float* src = p.part_o + (s * R + row) * D + lane * E;
 #pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = fmaf(x, __half2float(vp[k]), o[k] * a);
-    m = mn;
+    for (int k = 0; k < E; ++k) o[k] = fmaf(src[k], f, o[k]);
   }
+  const bool any = z > 0.0f || z != z;
 #pragma unroll
   for (int k = 0; k < E; ++k)
-    p.out[row * D + lane * E + k] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(z > 0.0f || z != z ? o[k] / z : 0.0f));
-  if (p.lse != nullptr && lane == 0) p.lse[row] = m + logf(z);
+    p.out[row * D + lane * E + k] = __bfloat16_as_ushort(__float2bfloat16_rn(any ? o[k] / z : 0.0f));
+  if (p.lse != nullptr && lane == 0)
+    p.lse[row] = any ? (m + log2f(z)) * 0.69314718f : -INFINITY;
+}
+
+// How the call is cut: row blocks per request and KV head, and splits of
+// the contexts.  A context is split while the blocks do not fill the SMs,
+// down to four tiles a split (below that the copies' latency and the join
+// outweigh what more CTAs bring).
+struct ChunkCut {
+  int mblocks, splits;
+};
+static ChunkCut chunk_cut(int B, int64_t n_tok, int Hq, int Hkv, int max_q, int max_len,
+                          int window) {
+  const int g = Hq / Hkv;
+  const int64_t q = max_q < n_tok ? max_q : n_tok;
+  ChunkCut c;
+  c.mblocks = (int)((q * g + 2 * kTile - 1) / (2 * kTile));
+  int64_t blocks = n_tok * g / (2 * kTile) + B;
+  if (blocks > (int64_t)B * c.mblocks) blocks = (int64_t)B * c.mblocks;
+  blocks *= Hkv;
+  int64_t span = max_len;
+  if (window > 0 && window + q < span) span = window + q;
+  const int64_t tiles = (span + kTile - 1) / kTile;
+  int64_t s = blocks > 0 ? num_sms() / blocks : 1;
+  if (s > tiles / 4) s = tiles / 4;
+  c.splits = (int)(s < 1 ? 1 : s);
+  return c;
 }
 
 int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
@@ -245,7 +688,9 @@ int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
 
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len) {
-  return chunk_layout(B, Hkv, d, chunk_cap_tiles(B, max_len, total_len)).total;
+  // without a window: a window only lowers the number of splits
+  const ChunkCut c = chunk_cut(B, n_tok, Hq, Hkv, max_q, max_len, 0);
+  return chunk_layout(B, n_tok * Hq, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.splits).total;
 }
 
 template <int D>
@@ -254,7 +699,9 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
   static unsigned long long attr_set = 0ull;
   if (device_needs_setup(&attr_set)) {
     if (cudaFuncSetAttribute(rebuild_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (3 * SDK_MAX_REQUESTS + 1) * 4) != cudaSuccess)
+                             (3 * SDK_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ACfg<D>::kSmem) != cudaSuccess)
       return SDK_ERR_CUDA;
     device_setup_done(&attr_set);
   }
@@ -262,17 +709,28 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
   if (grid > 8 * num_sms()) grid = 8 * num_sms();
   rebuild_kernel<D><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
-  const int64_t gx = ((int64_t)p.max_q * p.Hq + 3) / 4;
-  chunk_attn_kernel<D><<<dim3((unsigned)gx, (unsigned)p.B), 128, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SDK_OK : SDK_ERR_CUDA;
+  const int64_t ctas = (int64_t)p.B * p.Hkv * p.mblocks * p.splits;
+  if (ctas > 0x7FFFFFFF) return SDK_ERR_INVALID_ARG;
+  chunk_attn_kernel<D><<<(unsigned)ctas, kAThreads, ACfg<D>::kSmem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
+  if (p.splits > 1) {
+    chunk_join_kernel<D><<<(unsigned)((p.n_tok * p.Hq + 7) / 8), 256, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
+  }
+  return SDK_OK;
 }
 
 sdk_status launch_chunk_attn(ChunkParams p, char* workspace, cudaStream_t stream) {
-  const ChunkLayout l = chunk_layout(p.B, p.Hkv, p.d, p.cap_tiles);
+  const ChunkCut c = chunk_cut(p.B, p.n_tok, p.Hq, p.Hkv, p.max_q, p.max_len, p.window);
+  const ChunkLayout l = chunk_layout(p.B, p.n_tok * p.Hq, p.Hkv, p.d, p.cap_tiles, c.splits);
+  p.mblocks = c.mblocks;
+  p.splits = c.splits;
   p.hdr = reinterpret_cast<WsHeader*>(workspace);
   p.plan = reinterpret_cast<ReqPlan*>(workspace + l.plan);
   p.kt = reinterpret_cast<__half*>(workspace + l.kt);
   p.vt = reinterpret_cast<__half*>(workspace + l.vt);
+  p.part_ml = reinterpret_cast<float2*>(workspace + l.ml);
+  p.part_o = reinterpret_cast<float*>(workspace + l.po);
   return p.d == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
 }
 

@@ -55,9 +55,11 @@ struct ChunkParams {
   ReqPlan* plan;
   __half* kt;            // rebuilt key tiles [tile][Hkv][tile image]
   __half* vt;
+  float2* part_ml;       // partial sums of the splits [split][row][..]
+  float* part_o;
   int64_t n_tok;
   int B, Hq, Hkv, g, d, n, n_pages, page_size, max_pages;
-  int max_q, max_len, window, causal, cap_tiles;
+  int max_q, max_len, window, causal, cap_tiles, mblocks, splits;
   float scale;
 };
 
