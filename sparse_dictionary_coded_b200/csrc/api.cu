@@ -581,7 +581,7 @@ sdk_status sdk_chunk_attn(const void* q, int64_t n_tok, int32_t B, int32_t Hq, i
   p.causal = (flags & SDK_CHUNK_CAUSAL) ? 1 : 0;
   p.cap_tiles = (int)chunk_cap_tiles(B, max_len, total_len);
   p.scale = scale;
-  return launch_chunk_attn(p, reinterpret_cast<char*>(workspace),
+  return launch_chunk_attn(p, total_len, reinterpret_cast<char*>(workspace),
                            reinterpret_cast<cudaStream_t>(stream));
 }
 

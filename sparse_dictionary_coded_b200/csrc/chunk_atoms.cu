@@ -1,0 +1,865 @@
+// Chunk attention (sdk_chunk_attn) for few rows over long contexts, by
+// atoms instead of by rebuilt vectors:
+//   <q, K_t> = sum_j c_tj <q, D_K[i_tj]>           scores by 16 gathers
+//   sum_t p_t V_t = sum_a w_a D_V[a],  w_a = sum_t p_t sum_j c_tj [i_tj = a]
+// so a row costs 16 gathers and 16 additions a token in shared memory
+// (32768 atoms are 128 KB there), and the dictionaries are read once.
+//   atoms_qd_kernel     QD = D_K q^T, tcgen05: atoms on M, rows on N; fp16,
+//                       two rows side by side in one word per atom
+//   atoms_token_kernel  scores, softmax and weights of its share of the
+//                       (row pair, token) units, per segment of one pair
+//   atoms_out_kernel    w D_V, tcgen05, atoms split over the CTAs
+//   atoms_join_kernel   the segments' and atom ranges' sums, in fixed order
+#include "chunk_plan.cuh"
+#include "tc_ptx.cuh"
+
+namespace sdk {
+
+namespace {
+
+constexpr int kN = 128;            // rows per MMA tile
+constexpr int kM = 128;            // atoms per QD tile, head dims of w D_V
+constexpr int kChunk = 64;         // atoms per step of w D_V
+constexpr int kTab = SDK_MAX_ATOMS;
+constexpr int kTokThreads = 1024;
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct AtomCut {
+  int64_t pairs, work;             // bounds
+  int ctas, row_tiles, ksplits, chunks, n_pad;
+};
+
+AtomCut atom_cut(int B, int64_t n_tok, int Hq, int Hkv, int n, int max_q, int max_len,
+                 int64_t total_len) {
+  AtomCut c;
+  const int64_t g = Hq / Hkv, q = max_q < n_tok ? max_q : n_tok;
+  const int64_t each = (q * g + 1) / 2;                    // pairs of one request and KV head
+  c.pairs = (n_tok * g + B) / 2;                           // sum of ceil(n g / 2)
+  if (c.pairs > each * B) c.pairs = each * B;
+  c.pairs *= Hkv;
+  int64_t tokens = (int64_t)B * max_len;
+  if (total_len > 0 && total_len < tokens) tokens = total_len;
+  c.work = tokens * Hkv * each;
+  // a share below a thousand tokens would leave threads idle
+  const int64_t want = c.work / kTokThreads;
+  c.ctas = (int)(want < 1 ? 1 : want > num_sms() ? num_sms() : want);
+  // a segment is a CTA's share of one pair: at most ctas + pairs of them
+  c.row_tiles = (int)((2 * (c.ctas + c.pairs) + kN - 1) / kN);
+  c.chunks = (n + kChunk - 1) / kChunk;
+  int ks = num_sms() / c.row_tiles;
+  if (ks > c.chunks) ks = c.chunks;
+  c.ksplits = ks < 1 ? 1 : ks;
+  c.n_pad = (n + 3) / 4 * 4;                               // rows of QD in whole 16-byte pieces
+  return c;
+}
+
+struct AtomLayout {
+  size_t qd, scale, score, ml, w, o, total;
+};
+
+AtomLayout atom_layout(int B, int d, const AtomCut& c) {
+  AtomLayout l;
+  const size_t rows = (size_t)c.row_tiles * kN;
+  l.qd = up256(sizeof(WsHeader) + ((size_t)B + 1) * sizeof(ReqPlan));
+  l.scale = up256(l.qd + (size_t)c.pairs * c.n_pad * 4);
+  l.score = up256(l.scale + (size_t)c.pairs * 8);
+  l.ml = up256(l.score + (size_t)c.work * 8);
+  l.w = up256(l.ml + rows * 8);
+  l.o = up256(l.w + rows * c.chunks * kChunk * 2 * 2);
+  l.total = up256(l.o + (size_t)c.ksplits * rows * d * 4);
+  return l;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------- QD
+
+template <int D>
+struct QdCfg {
+  static constexpr int kStages = 3;
+  static constexpr int kStageB = kM * D * 2;
+  static constexpr int kOffB = kStages * kStageB;
+  static constexpr int kOffBar = kOffB + kN * D * 2;
+  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffRow = kOffMisc + 16;         // [kN] largest |q| of a column's row
+  static constexpr int kOffScan = kOffRow + kN * 4;     // [32] int64, then first pairs [B + 1]
+  static constexpr int kSmem = kOffScan + 256 + (SDK_MAX_REQUESTS + 1) * 4 + 1024;
+  static_assert(kSmem <= 232448, "exceeds the 227 KB shared memory of one sm_100 CTA");
+  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                                     ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+};
+
+// One CTA per (tile of 128 rows, strided set of 128-atom tiles): warp 0
+// streams the dictionary by TMA, warp 1 issues the MMAs (bf16 atoms and
+// queries, both exact, fp32 sums), warps 2-5 store.  A row is scaled by a
+// power of two that puts its largest entry in [1, 2), so fp16 holds
+// <q, d> with 11 significand bits for atoms of norm 1e-4 to 2900.  Bound by
+// the read of D_K and, with many rows, the stores of QD.
+template <int D>
+__global__ void __launch_bounds__(192, 1)
+    atoms_qd_kernel(const __grid_constant__ CUtensorMap kmap, ChunkParams p) {
+  using C = QdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = tc::align_smem_1k(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  uint32_t* s_max = reinterpret_cast<uint32_t*>(smem + C::kOffRow);
+  int64_t* s_warp = reinterpret_cast<int64_t*>(smem + C::kOffScan);
+  int32_t* s_pair0 = reinterpret_cast<int32_t*>(smem + C::kOffScan + 256);
+  volatile uint32_t* s_abort = misc;
+  volatile uint32_t* s_tmem = misc + 1;
+  const uint32_t s0 = tc::smem_u32(smem);
+  auto bar = [&](int i) { return tc::smem_u32(&bars[i]); };
+  auto bar_full = [&](int s) { return bar(s); };
+  auto bar_empty = [&](int s) { return bar(C::kStages + s); };
+  auto bar_tfull = [&](int b) { return bar(2 * C::kStages + b); };
+  auto bar_tempty = [&](int b) { return bar(2 * C::kStages + 2 + b); };
+  const uint32_t bar_done = bar(2 * C::kStages + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_tiles = (p.n + kM - 1) / kM;
+  if (tid == 0) {
+    *s_abort = 0u;
+    for (int i = 0; i < C::kNumBars; ++i)
+      tc::mbar_init(bar(i), i == 2 * C::kStages + 2 || i == 2 * C::kStages + 3 ? 4 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid < kN) s_max[tid] = 0u;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32((const void*)s_tmem)),
+                 "r"(2 * kN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  make_plan<true>(p, blockIdx.x == 0 && blockIdx.y == 0, s_pair0, s_warp);
+  const int n_pairs = s_pair0[p.B];
+  const int pair_base = blockIdx.y * (kN / 2);
+
+  // the tile's query rows as the K-major B operand (zero past the last)
+  for (int e = tid; e < kN * (D / 8); e += 192) {
+    const int col = e / (D / 8), kc = e % (D / 8);
+    const int pair = pair_base + col / 2;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (pair < n_pairs) {
+      const int b = find_first(s_pair0, p.B, pair);
+      const int row0 = p.cu_q[b], n = p.cu_q[b + 1] - row0;
+      const int npair = (int)(((int64_t)n * p.g + 1) / 2);
+      const int rel = pair - s_pair0[b], h = rel / npair;
+      const int r = (rel - h * npair) * 2 + (col & 1);
+      if (r < n * p.g) {
+        const int i = r / p.g;
+        const int64_t row = (int64_t)(row0 + i) * p.Hq + h * p.g + (r - i * p.g);
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + row * D) + kc);
+      }
+      uint32_t mx = 0u;
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mx = max(mx, max(x[u] & 0x7FFFu, (x[u] >> 16) & 0x7FFFu));
+      if (mx) atomicMax(&s_max[col], mx);
+    }
+    *reinterpret_cast<uint4*>(smem + C::kOffB + (kc >> 3) * (kN * 128) + col * 128 +
+                              (((kc & 7) ^ (col & 7)) << 4)) = v;
+  }
+  tc::fence_proxy_async();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  if (pair_base < n_pairs) {   // else nothing but the totals
+    if (blockIdx.x == 0 && tid < kN && pair_base + tid / 2 < n_pairs) {
+      float a, b;
+      row_scale(s_max[tid], 0, &a, &b);
+      p.row_scale[2 * pair_base + tid] = p.scale * 1.44269504f / a / b;
+    }
+    if (warp == 0) {
+      if (lane == 0) {
+        bool ok = true;
+        int k = 0;
+        for (int a = blockIdx.x; a < n_tiles; a += gridDim.x, ++k) {
+          const int st = k % C::kStages;
+          if (!tc::mbar_wait(bar_empty(st), ((uint32_t)(k / C::kStages) & 1u) ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_expect_tx(bar_full(st), (uint32_t)C::kStageB);
+#pragma unroll
+          for (int kb = 0; kb < D / 64; ++kb)
+            tc::tma_load_2d(s0 + st * C::kStageB + kb * (kM * 128), &kmap, kb * 64, a * kM,
+                            bar_full(st));
+        }
+        if (!ok) {
+          if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x60000000u | blockIdx.x);
+          *s_abort = 1u;
+        }
+        for (int i = max(0, k - C::kStages); i < k; ++i) {   // copies in flight land first
+          uint32_t never = 0u;
+          tc::mbar_wait(bar_full(i % C::kStages), (uint32_t)(i / C::kStages) & 1u, &never,
+                        100000000ull);
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        bool ok = true;
+        int k = 0;
+        for (int a = blockIdx.x; a < n_tiles; a += gridDim.x, ++k) {
+          const int st = k % C::kStages, tb = k & 1;
+          if (!tc::mbar_wait(bar_full(st), (uint32_t)(k / C::kStages) & 1u, s_abort) ||
+              !tc::mbar_wait(bar_tempty(tb), ((uint32_t)(k >> 1) & 1u) ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * (kM * 128) + (ks & 3) * 32;
+            tc::tc_mma(tmem + tb * kN, tc::smem_desc(s0 + st * C::kStageB + o),
+                       tc::smem_desc(s0 + C::kOffB + o), C::kIdesc, ks > 0);
+          }
+          tc::tc_commit(bar_empty(st));
+          tc::tc_commit(bar_tfull(tb));
+        }
+        if (!ok) {
+          if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x61000000u | blockIdx.x);
+          *s_abort = 1u;
+        }
+        tc::tc_commit(bar_done);
+        uint32_t never = 0u;
+        tc::mbar_wait(bar_done, 0u, &never, 100000000ull);
+      }
+      __syncwarp();
+    } else {
+      int k = 0;
+      const int live = min(kN, 2 * (n_pairs - pair_base));
+      for (int a = blockIdx.x; a < n_tiles; a += gridDim.x, ++k) {
+        const int tb = k & 1;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_tfull(tb), (uint32_t)(k >> 1) & 1u, s_abort))) {
+          if (lane == 0) {
+            if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x62000000u | blockIdx.x);
+            *s_abort = 1u;
+          }
+          break;
+        }
+        tc::tc_fence_after();
+        const int quarter = warp & 3;
+        const int atom = a * kM + quarter * 32 + lane;
+        bool over = false;
+        for (int cb = 0; cb < live; cb += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + tb * kN + cb, v);
+          tc::tmem_ld_wait();
+          if (atom < p.n_pad) {
+            __half2* dst = p.qd + (int64_t)(pair_base + cb / 2) * p.n_pad + atom;
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              if (cb + c >= live) break;
+              float x[2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                float f, f2;
+                row_scale(s_max[cb + c + u], 0, &f, &f2);
+                x[u] = __uint_as_float(v[c + u]) * f * f2;
+                if (fabsf(x[u]) > 65504.0f && !isinf(x[u])) {
+                  over = true;
+                  x[u] = copysignf(65504.0f, x[u]);
+                }
+              }
+              dst[(int64_t)(c / 2) * p.n_pad] = __floats2half2_rn(x[0], x[1]);
+            }
+          }
+        }
+        if (over) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x64000000u | (uint32_t)atom);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar_tempty(tb));
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kN)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- tokens
+
+namespace {
+
+// A token's position in the pages, stepped by kTokThreads without division.
+struct PageAt {
+  int col, off;
+  __device__ void init(int t, int P) {
+    col = t / P;
+    off = t - col * P;
+  }
+  __device__ void step(int dcol, int doff, int P) {
+    col += dcol;
+    off += doff;
+    if (off >= P) {
+      off -= P;
+      ++col;
+    }
+  }
+};
+
+template <typename T, typename F>
+__device__ __forceinline__ T block_reduce(T v, T* s_red, F f) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s_red[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// A code word made harmless: NaN coefficients 0, infinite ones +-65504.
+__device__ __forceinline__ uint32_t clean_word(uint32_t w, bool* bad) {
+  if ((w & 0x7C000000u) != 0x7C000000u) return w;
+  *bad = true;
+  if (w & 0x03FF0000u) return w & 0x7FFFu;
+  return (w & 0x80007FFFu) | 0x7BFF0000u;
+}
+
+}  // namespace
+
+// One CTA per SM takes an equal share of the (row pair, token) units, cut
+// into segments of one pair.  Per segment:
+//   1. QD of the pair (fp16, 128 KB) is copied to shared memory; a thread
+//      per token adds up 16 gathered products for both rows at once and
+//      keeps the scores in the workspace; the segment's maxima follow.
+//   2. For each row the table becomes the weights: 16 integer additions a
+//      token, p c in fixed point.  Integer sums make the result independent
+//      of the order of the atomics.  The point is set from a sample of the
+//      segment's values with a margin; the exact bound sum_t p_t sum_j |c_tj|
+//      is summed up on the way, and the row is redone with the point it
+//      gives should the margin not have held.
+//   3. The weights are written as two bf16 parts (16 significand bits) in
+//      the layout the product with D_V reads.
+// Bound by the shared memory: random gathers and additions of 32 lanes need
+// 3.5 passes over the banks on average.
+template <bool FULL>
+__global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams p) {
+  extern __shared__ __align__(16) uint32_t tab[];   // [kTab]
+  __shared__ float s_red[32];
+  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ uint32_t s_abort;
+  const int tid = threadIdx.x;
+  const int P = p.page_size;
+  const int dcol = kTokThreads / P, doff = kTokThreads - dcol * P;
+  const int64_t W = p.plan[p.B].work0;
+  int64_t w = W * blockIdx.x / gridDim.x;
+  const int64_t w_end = W * (blockIdx.x + 1) / gridDim.x;
+  if (w >= w_end) return;
+  int b;
+  {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.plan[mid].work0 <= w) lo = mid; else hi = mid;
+    }
+    b = lo;
+  }
+  if (tid == 0) {
+    s_abort = 0u;
+    tc::mbar_init(tc::smem_u32(&s_bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  uint32_t parity = 0;
+  auto fmax2 = [](float a, float c) { return fmaxf(a, c); };
+  auto fadd2 = [](float a, float c) { return a + c; };
+  while (w < w_end) {
+    while (p.plan[b + 1].work0 <= w) ++b;     // p.plan[B] holds the totals
+    const ReqPlan rp = p.plan[b];
+    const int span = rp.len - rp.lo;
+    const int64_t q = (w - rp.work0) / span;
+    const int u0 = (int)(w - rp.work0 - q * span);
+    const int cnt = (int)min((int64_t)(span - u0), w_end - w);
+    const int h = (int)(q / rp.npair), j = (int)(q - (int64_t)h * rp.npair);
+    const int pair = rp.pair0 + (int)q;
+    const int slot = (int)blockIdx.x + pair;
+    const int ta = rp.lo + u0, tb = ta + cnt;
+    float2* score = p.score + w;
+    const int32_t* table = p.table + (int64_t)b * p.max_pages;
+
+    tc::fence_proxy_async();
+    __syncthreads();                          // the table is free
+    if (tid == 0) {
+      tc::mbar_expect_tx(tc::smem_u32(&s_bar), (uint32_t)p.n_pad * 4u);
+      bulk_load(tc::smem_u32(tab), p.qd + (int64_t)pair * p.n_pad, (uint32_t)p.n_pad * 4u,
+                tc::smem_u32(&s_bar));
+    }
+    if (!FULL)
+      for (int a = p.n_pad + tid; a < kTab; a += kTokThreads) tab[a] = 0u;
+    // what the two rows see
+    int see0[2], see1[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * j + e, pos = rp.len - rp.n + r / p.g;
+      const bool live = r < rp.n * p.g;
+      see1[e] = !live ? -1 : p.causal ? min(pos, rp.len - 1) : rp.len - 1;
+      see0[e] = p.window > 0 ? pos - p.window + 1 : 0;
+    }
+    const float sc0 = p.row_scale[2 * pair], sc1 = p.row_scale[2 * pair + 1];
+    const bool got = tc::mbar_wait(tc::smem_u32(&s_bar), parity, &s_abort);
+    parity ^= 1u;
+    if (!__syncthreads_and(got)) {
+      if (tid == 0) {
+        record_error(p.hdr, SDK_ERR_TIMEOUT, 0x65000000u | blockIdx.x);
+        uint32_t never = 0u;                  // the copy lands before the CTA leaves
+        tc::mbar_wait(tc::smem_u32(&s_bar), parity ^ 1u, &never, 100000000ull);
+      }
+      return;
+    }
+
+    // ---- scores
+    float m0 = -INFINITY, m1 = -INFINITY;
+    bool nan0 = false, nan1 = false;
+    uint32_t top = 0u;                        // largest atom index met
+    PageAt at;
+    at.init(min(ta + tid, rp.len), P);
+    for (int t = ta + tid; t < tb; t += kTokThreads, at.step(dcol, doff, P)) {
+      const int page = table[at.col];
+      float a0 = 0.0f, a1 = 0.0f;
+      if (page >= 0 && page < p.n_pages) {
+        const uint4* rec = reinterpret_cast<const uint4*>(
+            p.pages + (((int64_t)page * p.Hkv + h) * P + at.off) * 2 * kAtoms);
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = __ldg(rec + k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a = word_idx(ws[i]);
+            const float2 qd = __half22float2(*reinterpret_cast<const __half2*>(tab + a));
+            const float c = word_coef(ws[i]);
+            a0 = fmaf(c, qd.x, a0);
+            a1 = fmaf(c, qd.y, a1);
+            if (!FULL) top = max(top, a);
+          }
+        }
+        if (!(fabsf(a0) < INFINITY) || !(fabsf(a1) < INFINITY)) {
+          // a bad word, or a bad query row: the words are made harmless
+          bool bad = false;
+          a0 = a1 = 0.0f;
+          for (int k = 0; k < kAtoms; ++k) {
+            const uint32_t y =
+                clean_word(__ldg(reinterpret_cast<const uint32_t*>(rec) + k), &bad);
+            const float2 qd = __half22float2(*reinterpret_cast<const __half2*>(tab + word_idx(y)));
+            a0 = fmaf(word_coef(y), qd.x, a0);
+            a1 = fmaf(word_coef(y), qd.y, a1);
+          }
+          if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
+        }
+      } else {
+        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
+      }
+      a0 = t >= see0[0] && t <= see1[0] ? a0 * sc0 : -INFINITY;
+      a1 = t >= see0[1] && t <= see1[1] ? a1 * sc1 : -INFINITY;
+      nan0 |= a0 != a0;
+      nan1 |= a1 != a1;
+      m0 = fmaxf(m0, a0);
+      m1 = fmaxf(m1, a1);
+      score[t - ta] = make_float2(a0, a1);
+    }
+    if (!FULL && top >= (uint32_t)p.n)
+      record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
+    const bool row_nan0 = __syncthreads_or(nan0) != 0, row_nan1 = __syncthreads_or(nan1) != 0;
+    m0 = block_reduce(m0, s_red, fmax2);
+    m1 = block_reduce(m1, s_red, fmax2);
+
+    // ---- weights, row by row
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      if (2 * j + e >= rp.n * p.g) break;
+      const float m = e ? m1 : m0;
+      const int row = 2 * slot + e;
+      const bool isnan_row = e ? row_nan1 : row_nan0;
+      if (isnan_row || m == -INFINITY || m == INFINITY) {
+        // nothing seen (0), or a row that is NaN whatever its values are
+        if (tid == 0)
+          p.part_ml[row] = isnan_row || m == INFINITY
+                               ? make_float2(0.0f, __int_as_float(0x7FC00000))
+                               : make_float2(-INFINITY, 0.0f);
+        continue;
+      }
+      // the size of p c from one token per thread; only tokens that the row
+      // sees have a say in its rounding
+      float sa = 0.0f, sp = 0.0f, spa = 0.0f;
+      at.init(min(ta + tid, rp.len), P);
+      if (tid < cnt) {
+        const float2 s2 = score[tid];
+        sp = ex2((e ? s2.y : s2.x) - m);
+        const int page = table[at.col];
+        if (sp > 0.0f && page >= 0 && page < p.n_pages) {
+          const uint32_t* rec =
+              p.pages + ((((int64_t)page * p.Hkv + h) * P + at.off) * 2 + 1) * kAtoms;
+          for (int k = 0; k < kAtoms; ++k) sa += fabsf(word_coef(rec[k]));
+          spa = sp * sa;
+        }
+      }
+      const float seen = (float)max(1, __syncthreads_count(sp > 0.0f));
+      sa = block_reduce(sa, s_red, fadd2);
+      sp = block_reduce(sp, s_red, fadd2);
+      spa = block_reduce(spa, s_red, fadd2);
+      float bound = 8.0f * fmaxf(sa / seen, fmaxf(spa, sp * (sa / seen)) / (float)min(cnt, kTokThreads) *
+                                                (float)cnt);
+      float z = 0.0f, inv = 0.0f;
+      bool clean = false;
+#pragma unroll 1
+      for (int attempt = 0; attempt < 3; ++attempt) {
+        // |w| <= bound: the point that puts bound below 2^30
+        if (!(bound > 1e-30f)) bound = 1e-30f;
+        if (!(bound < 1e30f)) bound = 1e30f;
+        const int ex = (int)((__float_as_uint(bound) >> 23) & 255u) - 127 + 1;   // bound < 2^ex
+        const float up = __uint_as_float((uint32_t)(min(30 - ex, 126) + 127) << 23);
+        inv = 1.0f / up;
+        __syncthreads();
+        for (int a = tid; a < kTab / 4; a += kTokThreads)
+          reinterpret_cast<uint4*>(tab)[a] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        float za = 0.0f, aa = 0.0f;
+        uint32_t vtop = 0u;
+        at.init(min(ta + tid, rp.len), P);
+        for (int t = ta + tid; t < tb; t += kTokThreads, at.step(dcol, doff, P)) {
+          const float2 s2 = score[t - ta];
+          const float pr = ex2((e ? s2.y : s2.x) - m);
+          za += pr;
+          const int page = table[at.col];
+          if (!(pr > 0.0f) || page < 0 || page >= p.n_pages) continue;
+          const uint4* rec = reinterpret_cast<const uint4*>(
+              p.pages + ((((int64_t)page * p.Hkv + h) * P + at.off) * 2 + 1) * kAtoms);
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = __ldg(rec + k);
+          const float pu = pr * up;
+          float ca = 0.0f;
+          bool bad = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (clean) ws[i] = clean_word(ws[i], &bad);
+              const uint32_t a = word_idx(ws[i]);
+              const float c = word_coef(ws[i]);
+              ca += fabsf(c);
+              const int add = __float2int_rn(pu * c);
+              if (add != 0) atomicAdd(reinterpret_cast<int*>(tab) + a, add);
+              if (!FULL) vtop = max(vtop, a);
+            }
+          }
+          aa = fmaf(pr, ca, aa);
+          if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
+        }
+        if (!FULL && vtop >= (uint32_t)p.n)
+          record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
+        z = block_reduce(za, s_red, fadd2);
+        aa = block_reduce(aa, s_red, fadd2);
+        if (aa * up < 2.0e9f) break;          // every sum fits (false for NaN)
+        if (!(aa < INFINITY)) {
+          clean = true;
+          bound = 0.0f;                       // the next attempt only finds the bound
+        } else {
+          bound = aa * 1.01f;
+        }
+      }
+      __syncthreads();
+      if (tid == 0) p.part_ml[row] = make_float2(m, z);
+      // [row tile][chunk][part][128 rows][64 atoms], 128-byte swizzle
+      const int chunks = (p.n + kChunk - 1) / kChunk;
+      char* img = p.wimg + (int64_t)(row / kN) * chunks * 2 * (kN * 128) + (row % kN) * 128;
+      for (int o = tid; o < chunks * 8; o += kTokThreads) {
+        const int4 v0 = reinterpret_cast<const int4*>(tab)[2 * o];
+        const int4 v1 = reinterpret_cast<const int4*>(tab)[2 * o + 1];
+        const int v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float f[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            f[s] = FULL || 8 * o + 2 * u + s < p.n ? (float)v[2 * u + s] * inv : 0.0f;
+          const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]);
+          const __nv_bfloat162 c =
+              __floats2bfloat162_rn(f[0] - __low2float(a), f[1] - __high2float(a));
+          hi[u] = *reinterpret_cast<const uint32_t*>(&a);
+          lo[u] = *reinterpret_cast<const uint32_t*>(&c);
+        }
+        char* dst = img + (int64_t)(o >> 3) * 2 * (kN * 128) + (((o & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + kN * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    w += cnt;
+  }
+}
+
+// ------------------------------------------------------------------ w D_V
+
+struct OutCfg {
+  static constexpr int kStages = 4;
+  static constexpr int kA = kM * kChunk * 2;               // D_V chunk, two halves of 64 dims
+  static constexpr int kB = 2 * kN * kChunk * 2;           // both parts of w
+  static constexpr int kStage = kA + kB;
+  static constexpr int kOffBar = kStages * kStage;
+  static constexpr int kSmem = kOffBar + (2 * kStages + 1) * 8 + 16 + 1024;
+  static_assert(kSmem <= 232448, "exceeds the 227 KB shared memory of one sm_100 CTA");
+  // A (D_V) MN-major, B (w) K-major, both bf16
+  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) |
+                                     ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+};
+
+// out^T = D_V^T w^T for a tile of 128 rows over the CTA's atom range: head
+// dims on M, rows on N, both operands by bulk and TMA copies; the partial
+// sums go to the workspace.  Bound by the copies of w (4 bytes an atom and
+// row) and D_V from L2.
+template <int D>
+__global__ void __launch_bounds__(128, 1)
+    atoms_out_kernel(const __grid_constant__ CUtensorMap vmap, ChunkParams p) {
+  using C = OutCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = tc::align_smem_1k(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * C::kStages + 1);
+  volatile uint32_t* s_abort = misc;
+  volatile uint32_t* s_tmem = misc + 1;
+  const uint32_t s0 = tc::smem_u32(smem);
+  auto bar_full = [&](int s) { return tc::smem_u32(&bars[s]); };
+  auto bar_empty = [&](int s) { return tc::smem_u32(&bars[C::kStages + s]); };
+  const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages]);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // rows that no segment wrote are not read
+  const int rows = 2 * (p.ctas + p.plan[p.B].pair0);
+  if ((int)blockIdx.y * kN >= rows) return;
+  const int chunks = (p.n + kChunk - 1) / kChunk;
+  const int c0 = (int)((int64_t)chunks * blockIdx.x / gridDim.x);
+  const int c1 = (int)((int64_t)chunks * (blockIdx.x + 1) / gridDim.x);
+  if (tid == 0) {
+    *s_abort = 0u;
+    for (int i = 0; i <= 2 * C::kStages; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32((const void*)s_tmem)),
+                 "r"(kN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (D < kM) {
+    // 64-dim heads: the upper half of every D_V stage stays zero
+    for (int s = 0; s < C::kStages; ++s)
+      for (int e = tid; e < C::kA / 32; e += 128)
+        reinterpret_cast<uint4*>(smem + s * C::kStage + C::kA / 2)[e] = make_uint4(0u, 0u, 0u, 0u);
+    tc::fence_proxy_async();
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  if (warp == 0) {
+    if (lane == 0) {
+      const char* img = p.wimg + ((int64_t)blockIdx.y * chunks + c0) * C::kB;
+      bool ok = true;
+      int k = 0;
+      for (; k < c1 - c0; ++k) {
+        const int st = k % C::kStages;
+        if (!tc::mbar_wait(bar_empty(st), ((uint32_t)(k / C::kStages) & 1u) ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = s0 + st * C::kStage;
+        tc::mbar_expect_tx(bar_full(st), (uint32_t)(D * kChunk * 2 + C::kB));
+        tc::tma_load_2d(sa, &vmap, 0, (c0 + k) * kChunk, bar_full(st));
+        if (D > 64) tc::tma_load_2d(sa + C::kA / 2, &vmap, 64, (c0 + k) * kChunk, bar_full(st));
+        bulk_load(sa + C::kA, img + (int64_t)k * C::kB, (uint32_t)C::kB, bar_full(st));
+      }
+      if (!ok) {
+        if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x66000000u | blockIdx.x);
+        *s_abort = 1u;
+      }
+      for (int i = max(0, k - C::kStages); i < k; ++i) {
+        uint32_t never = 0u;
+        tc::mbar_wait(bar_full(i % C::kStages), (uint32_t)(i / C::kStages) & 1u, &never,
+                      100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int k = 0; k < c1 - c0; ++k) {
+        const int st = k % C::kStages;
+        if (!tc::mbar_wait(bar_full(st), (uint32_t)(k / C::kStages) & 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t sa = s0 + st * C::kStage, sb = sa + C::kA;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int ks = 0; ks < kChunk / 16; ++ks)
+            tc::tc_mma(tmem, tc::smem_desc_mn(sa + ks * 2048, C::kA / 2, 1024u),
+                       tc::smem_desc(sb + part * (kN * 128) + ks * 32), C::kIdesc,
+                       k > 0 || part > 0 || ks > 0);
+        tc::tc_commit(bar_empty(st));
+      }
+      if (!ok) {
+        if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x67000000u | blockIdx.x);
+        *s_abort = 1u;
+      }
+      tc::tc_commit(bar_done);
+    }
+  }
+  __syncwarp();
+  uint32_t never = 0u;
+  const bool done = __all_sync(0xffffffffu, tc::mbar_wait(bar_done, 0u, &never));
+  if (!done && lane == 0) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x68000000u | blockIdx.x);
+  tc::tc_fence_after();
+  const int dim = warp * 32 + lane;
+  float* dst = p.part_o + ((int64_t)blockIdx.x * p.row_tiles + blockIdx.y) * kN * D + dim;
+  if (done && warp * 32 < D) {
+    for (int cb = 0; cb < kN && (int)blockIdx.y * kN + cb < rows; cb += 32) {
+      uint32_t v[32];
+      tc::tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + cb, v);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) dst[(int64_t)(cb + c) * D] = __uint_as_float(v[c]);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kN)
+                 : "memory");
+  }
+}
+
+// The sums of a row's segments over all atom ranges; a thread per dim.
+template <int D>
+__global__ void __launch_bounds__(128) atoms_join_kernel(ChunkParams p) {
+  const int64_t row = (int64_t)blockIdx.x * (128 / D) + threadIdx.x / D;
+  const int dim = threadIdx.x % D;
+  if (row >= p.n_tok * p.Hq) return;
+  const int tok = (int)(row / p.Hq), hq = (int)(row - (int64_t)tok * p.Hq);
+  const ReqPlan rp = p.plan[find_request(p, tok)];
+  // rows of no request, or of a refused one, stay as they were
+  if (tok < rp.row0 || tok >= rp.row0 + rp.n) return;
+  const int h = hq / p.g, r = (tok - rp.row0) * p.g + (hq - h * p.g);
+  const int64_t q = (int64_t)h * rp.npair + (r >> 1), span = rp.len - rp.lo;
+  const int64_t w0 = rp.work0 + q * span, w1 = w0 + span, W = p.plan[p.B].work0;
+  const int pair = rp.pair0 + (int)q;
+  float m = -INFINITY, z = 0.0f, o = 0.0f;
+  if (span > 0) {
+    int c0 = (int)((double)w0 / (double)W * p.ctas);
+    c0 = min(max(c0, 0), p.ctas - 1);
+    while (c0 > 0 && W * c0 / p.ctas > w0) --c0;
+    while (c0 + 1 < p.ctas && W * (c0 + 1) / p.ctas <= w0) ++c0;
+    const int64_t rows = (int64_t)p.row_tiles * kN;
+    for (int pass = 0; pass < 2; ++pass)
+      for (int c = c0; c < p.ctas; ++c) {
+        const int64_t a = max(w0, W * c / p.ctas), e = min(w1, W * (c + 1) / p.ctas);
+        if (W * c / p.ctas >= w1) break;
+        if (a >= e) continue;
+        const int64_t i = 2 * (int64_t)(c + pair) + (r & 1);
+        const float2 ml = p.part_ml[i];
+        if (pass == 0) {
+          m = fmaxf(m, ml.x);
+        } else if (!(ml.x == -INFINITY && ml.y == 0.0f)) {   // else it saw nothing
+          const float f = ex2(ml.x - m);
+          z = fmaf(ml.y, f, z);
+          float s = 0.0f;
+          for (int k = 0; k < p.ksplits; ++k) s += p.part_o[(k * rows + i) * D + dim];
+          o = fmaf(s, f, o);
+        }
+      }
+  }
+  const bool any = z > 0.0f || z != z;
+  p.out[row * D + dim] =
+      __bfloat16_as_ushort(__float2bfloat16_rn(z != z ? z : any ? o / z : 0.0f));
+  if (p.lse != nullptr && dim == 0) p.lse[row] = any ? (m + log2f(z)) * 0.69314718f : -INFINITY;
+}
+
+// ------------------------------------------------------------------- host
+
+size_t atoms_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
+                             int max_len, int64_t total_len) {
+  return atom_layout(B, d, atom_cut(B, n_tok, Hq, Hkv, n, max_q, max_len, total_len)).total;
+}
+
+template <int D>
+static sdk_status launch_atoms_d(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 const ChunkParams& p, cudaStream_t stream) {
+  static unsigned long long attr_set = 0ull;
+  if (device_needs_setup(&attr_set)) {
+    if (cudaFuncSetAttribute(atoms_qd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             QdCfg<D>::kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(atoms_token_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kTab * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(atoms_token_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kTab * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(atoms_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             OutCfg::kSmem) != cudaSuccess)
+      return SDK_ERR_CUDA;
+    device_setup_done(&attr_set);
+  }
+  const int tiles = (p.n + kM - 1) / kM;
+  const unsigned ty = (unsigned)((2 * p.cap_pairs + kN - 1) / kN);
+  unsigned gx = (unsigned)num_sms() / ty;
+  gx = gx < 1 ? 1 : gx > (unsigned)tiles ? (unsigned)tiles : gx;
+  atoms_qd_kernel<D><<<dim3(gx, ty), 192, QdCfg<D>::kSmem, stream>>>(kmap, p);
+  if (p.n == kTab)
+    atoms_token_kernel<true><<<p.ctas, kTokThreads, kTab * 4, stream>>>(p);
+  else
+    atoms_token_kernel<false><<<p.ctas, kTokThreads, kTab * 4, stream>>>(p);
+  atoms_out_kernel<D><<<dim3((unsigned)p.ksplits, (unsigned)p.row_tiles), 128, OutCfg::kSmem,
+                        stream>>>(vmap, p);
+  const int64_t per = 128 / D;
+  atoms_join_kernel<D><<<(unsigned)((p.n_tok * p.Hq + per - 1) / per), 128, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SDK_OK : SDK_ERR_CUDA;
+}
+
+sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
+                              cudaStream_t stream, bool* taken) {
+  *taken = false;
+  auto fn = tc::encode_fn();
+  if (fn == nullptr) return SDK_OK;
+  CUtensorMap maps[2];
+  for (int s = 0; s < 2; ++s) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.d, (cuuint64_t)p.n};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.d * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)(s == 0 ? kM : kChunk)};
+    const cuuint32_t estr[2] = {1u, 1u};
+    if (fn(&maps[s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+           const_cast<uint16_t*>(s == 0 ? p.dk : p.dv), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return SDK_OK;
+  }
+  *taken = true;
+  const AtomCut c = atom_cut(p.B, p.n_tok, p.Hq, p.Hkv, p.n, p.max_q, p.max_len, total_len);
+  const AtomLayout l = atom_layout(p.B, p.d, c);
+  p.cap_pairs = c.pairs;
+  p.cap_work = c.work;
+  p.ctas = c.ctas;
+  p.row_tiles = c.row_tiles;
+  p.ksplits = c.ksplits;
+  p.n_pad = c.n_pad;
+  p.qd = reinterpret_cast<__half2*>(workspace + l.qd);
+  p.row_scale = reinterpret_cast<float*>(workspace + l.scale);
+  p.score = reinterpret_cast<float2*>(workspace + l.score);
+  p.part_ml = reinterpret_cast<float2*>(workspace + l.ml);
+  p.wimg = workspace + l.w;
+  p.part_o = reinterpret_cast<float*>(workspace + l.o);
+  return p.d == 128 ? launch_atoms_d<128>(maps[0], maps[1], p, stream)
+                    : launch_atoms_d<64>(maps[0], maps[1], p, stream);
+}
+
+}  // namespace sdk

@@ -4,14 +4,13 @@
 //   K_t = sum_j c_tj D_K[i_tj],  V_t = sum_j c_tj D_V[i_tj]
 // once per call as fp16 tiles of 128 tokens in the workspace, and
 // chunk_attn_kernel computes softmax(scale q K^T) V over the tiles.
-#include "paged.cuh"
+#include "chunk_plan.cuh"
 #include "tc_ptx.cuh"
 
 namespace sdk {
 
 namespace {
 
-constexpr int kTile = 128;        // tokens of a rebuilt tile
 constexpr int kRebThreads = 256;
 constexpr int kRebTok = 32;       // tokens of one work item of rebuild_kernel
 
@@ -25,7 +24,7 @@ ChunkLayout chunk_layout(int B, int64_t rows, int Hkv, int d, int64_t cap_tiles,
   ChunkLayout l;
   const size_t tiles = (size_t)cap_tiles * Hkv * kTile * d * 2;
   l.plan = sizeof(WsHeader);
-  l.kt = up256(l.plan + (size_t)B * sizeof(ReqPlan));
+  l.kt = up256(l.plan + ((size_t)B + 1) * sizeof(ReqPlan));
   l.vt = l.kt + tiles;
   l.ml = l.vt + tiles;
   const size_t parts = splits > 1 ? (size_t)splits * rows : 0;
@@ -55,60 +54,9 @@ template <int D>
 __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
   extern __shared__ int32_t sm[];
   int32_t* s_tile0 = sm;              // [B + 1]
-  int32_t* s_lo = s_tile0 + p.B + 1;  // [B]
-  int32_t* s_len = s_lo + p.B;        // [B]
-  __shared__ uint32_t s_warp[32];
+  __shared__ int64_t s_warp[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t base = 0;
-  if (tid == 0) s_tile0[0] = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kRebThreads) {
-    const int b = b0 + tid;
-    int row0 = 0, n = 0, len = 0, lo = 0;
-    uint32_t nt = 0, err = 0;
-    if (b < p.B) {
-      row0 = p.cu_q[b];
-      const int row1 = p.cu_q[b + 1];
-      len = p.lens[b];
-      if (row0 < 0 || row1 < row0 || row1 > p.n_tok || len < 0) {
-        err = SDK_ERR_DEVICE_CHECK;
-      } else if (row1 - row0 > p.max_q || len > p.max_len) {
-        err = SDK_ERR_CAPACITY;
-      } else {
-        n = row1 - row0;
-      }
-      if (n > 0) {
-        // the first row's position len - n sees tokens from len - n - window + 1 on
-        if (p.window > 0) lo = max(0, (int)max((int64_t)len - n - p.window + 1, (int64_t)0));
-        lo = lo / kTile * kTile;
-        nt = (uint32_t)((max(len - lo, 0) + kTile - 1) / kTile);
-      }
-    }
-    uint32_t total;
-    const uint32_t upto = base + block_incl_scan(nt, s_warp, &total);
-    if (b < p.B) {
-      if (upto > (uint32_t)p.cap_tiles && nt > 0) {   // total_len does not hold
-        err = SDK_ERR_CAPACITY;
-        n = 0;
-      }
-      s_tile0[b + 1] = (int)min(upto, (uint32_t)p.cap_tiles);
-      s_lo[b] = lo;
-      s_len[b] = n > 0 ? len : 0;
-      if (blockIdx.x == 0) {
-        ReqPlan r;
-        r.row0 = row0;
-        r.n = n;
-        r.len = len;
-        r.lo = lo;
-        r.tile0 = (int)(upto - nt);
-        r.ntiles = n > 0 ? (int)nt : 0;
-        r.pad[0] = r.pad[1] = 0;
-        p.plan[b] = r;
-        if (err) record_error(p.hdr, err, 0x75000000u | (uint32_t)b);
-      }
-    }
-    base += total;
-  }
-  __syncthreads();
+  make_plan<false>(p, blockIdx.x == 0, s_tile0, s_warp);
 
   constexpr int LPR = D / 8;           // lanes per record
   constexpr int TPS = 32 / (2 * LPR);  // tokens a warp rebuilds at a time
@@ -124,21 +72,20 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
     const int64_t th = it / (kTile / kRebTok);
     const int h = (int)(th % p.Hkv);
     const int tile = (int)(th / p.Hkv);
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_tile0[mid] <= tile) lo = mid; else hi = mid;
-    }
-    const int b = lo;
+    const int b = find_first(s_tile0, p.B, tile);
+    unsigned err;
+    const ReqPlan rq = check_request(p, b, &err);
+    const int t_tile = rq.lo + (tile - s_tile0[b]) * kTile;
+    const int t_end = rq.n > 0 ? rq.len : 0;
     char* dst = tiles + ((int64_t)tile * p.Hkv + h) * (kTile * D * 2);
 #pragma unroll 1
     for (int u = 0; u < kTokWarp; u += TPS) {
       const int r = part * kRebTok + warp * kTokWarp + u + (rec >> 1);   // row of the tile
-      const int t = s_lo[b] + (tile - s_tile0[b]) * kTile + r;
+      const int t = t_tile + r;
       uint32_t w[WPL];
 #pragma unroll
       for (int i = 0; i < WPL; ++i) w[i] = 0u;
-      if (t < s_len[b]) {
+      if (t < t_end) {
         const int col = t / p.page_size, off = t - col * p.page_size;
         const int page = p.table[(int64_t)b * p.max_pages + col];
         if (page >= 0 && page < p.n_pages) {
@@ -242,12 +189,6 @@ struct ACfg {
                                       ((uint32_t)(kTile >> 4) << 24);
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   const uint32_t z = 0u;
@@ -274,15 +215,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
 }
 
 }  // namespace
@@ -458,12 +390,8 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
 #pragma unroll
         for (int u = 0; u < 4; ++u) mx = max(mx, max(x[u] & 0x7FFFu, (x[u] >> 16) & 0x7FFFu));
       }
-      // 2^e q: the largest entry's exponent becomes 14 (e = 0 for a row of
-      // zeros or one with infinities or NaN, which spoil that row alone)
-      int e = (mx >> 7) == 0u || (mx >> 7) == 255u ? 0 : 14 + 127 - (int)(mx >> 7);
-      if (mx != 0u && (mx >> 7) == 0u) e = 126;    // subnormal: as far as one factor goes
-      const float up = __uint_as_float((uint32_t)(min(e, 126) + 127) << 23);
-      const float up2 = __uint_as_float((uint32_t)(max(e - 126, 0) + 127) << 23);
+      float up, up2;
+      row_scale(mx, 14, &up, &up2);
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
         const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -625,12 +553,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
   const int lane = threadIdx.x & 31;
   // rows of no request, or of a refused one, stay as they were
   const int tok = (int)(row / p.Hq);
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_q[mid] <= tok) lo = mid; else hi = mid;
-  }
-  const ReqPlan rp = p.plan[lo];
+  const ReqPlan rp = p.plan[find_request(p, tok)];
   if (row >= R || tok < rp.row0 || tok >= rp.row0 + rp.n) return;
   float m = -INFINITY;
   for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[s * R + row].x);
@@ -686,21 +609,35 @@ int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
   return sum < each ? sum : each;
 }
 
+// Which form a call takes.  Rebuilding costs 0.74 ns a token and KV head
+// (head_dim 128), however many rows follow; going by atoms costs PER_PAIR
+// for every two rows and FIXED once.
+static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q, int max_len,
+                     int64_t total_len) {
+  const int64_t q = max_q < n_tok ? max_q : n_tok;
+  const int64_t pairs = (q * (Hq / Hkv) + 1) / 2;
+  const int64_t tokens = (total_len > 0 ? total_len : (int64_t)B * max_len) * Hkv;
+  if (q < 1) return false;
+  return pairs <= 8 && tokens >= 65536;
+}
+
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len) {
   // without a window: a window only lowers the number of splits
   const ChunkCut c = chunk_cut(B, n_tok, Hq, Hkv, max_q, max_len, 0);
-  return chunk_layout(B, n_tok * Hq, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.splits).total;
+  const size_t a =
+      chunk_layout(B, n_tok * Hq, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.splits).total;
+  if (!by_atoms(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len)) return a;
+  const size_t b = atoms_workspace_bytes(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
+  return a > b ? a : b;
 }
 
 template <int D>
 static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
-  const size_t smem = (size_t)(3 * p.B + 1) * 4;
+  const size_t smem = (size_t)(p.B + 1) * 4;
   static unsigned long long attr_set = 0ull;
   if (device_needs_setup(&attr_set)) {
-    if (cudaFuncSetAttribute(rebuild_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (3 * SDK_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
-        cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ACfg<D>::kSmem) != cudaSuccess)
       return SDK_ERR_CUDA;
     device_setup_done(&attr_set);
@@ -720,13 +657,19 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
   return SDK_OK;
 }
 
-sdk_status launch_chunk_attn(ChunkParams p, char* workspace, cudaStream_t stream) {
+sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
+                             cudaStream_t stream) {
+  p.hdr = reinterpret_cast<WsHeader*>(workspace);
+  p.plan = reinterpret_cast<ReqPlan*>(workspace + sizeof(WsHeader));
+  if (by_atoms(p.B, p.n_tok, p.Hq, p.Hkv, p.d, p.n, p.max_q, p.max_len, total_len)) {
+    bool taken = false;
+    const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
+    if (taken) return s;
+  }
   const ChunkCut c = chunk_cut(p.B, p.n_tok, p.Hq, p.Hkv, p.max_q, p.max_len, p.window);
   const ChunkLayout l = chunk_layout(p.B, p.n_tok * p.Hq, p.Hkv, p.d, p.cap_tiles, c.splits);
   p.mblocks = c.mblocks;
   p.splits = c.splits;
-  p.hdr = reinterpret_cast<WsHeader*>(workspace);
-  p.plan = reinterpret_cast<ReqPlan*>(workspace + l.plan);
   p.kt = reinterpret_cast<__half*>(workspace + l.kt);
   p.vt = reinterpret_cast<__half*>(workspace + l.vt);
   p.part_ml = reinterpret_cast<float2*>(workspace + l.ml);

@@ -1,0 +1,158 @@
+// The plan of a chunk attention call, made on the device from the requests'
+// lengths: checked bounds and running sums, the same for every CTA.
+#pragma once
+
+#include "paged.cuh"
+
+namespace sdk {
+
+constexpr int kTile = 128;   // tokens of a rebuilt tile; a request's first token rounds down to one
+
+// Inclusive scan of one 64-bit value per thread (blockDim.x a multiple of
+// 32, <= 1024).
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* s_warp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t t = lane < nw ? s_warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += u;
+    }
+    if (lane < nw) s_warp[lane] = t;
+  }
+  __syncthreads();
+  const int64_t r = warp > 0 ? v + s_warp[warp - 1] : v;
+  *total = s_warp[nw - 1];
+  __syncthreads();
+  return r;
+}
+
+// Checks request b's offsets and lengths; n = 0 refuses it (err says why).
+__device__ __forceinline__ ReqPlan check_request(const ChunkParams& p, int b, unsigned* err) {
+  ReqPlan r = {};
+  r.row0 = p.cu_q[b];
+  const int row1 = p.cu_q[b + 1];
+  r.len = p.lens[b];
+  *err = 0;
+  if (r.row0 < 0 || row1 < r.row0 || row1 > p.n_tok || r.len < 0)
+    *err = SDK_ERR_DEVICE_CHECK;
+  else if (row1 - r.row0 > p.max_q || r.len > p.max_len)
+    *err = SDK_ERR_CAPACITY;
+  else
+    r.n = row1 - r.row0;
+  if (r.n > 0) {
+    // the first row's position len - n sees tokens from len - n - window + 1 on
+    if (p.window > 0) r.lo = (int)max((int64_t)r.len - r.n - p.window + 1, (int64_t)0);
+    r.lo = min(r.lo, r.len) / kTile * kTile;
+    r.ntiles = (r.len - r.lo + kTile - 1) / kTile;
+    r.npair = (int)(((int64_t)r.n * p.g + 1) / 2);
+  }
+  return r;
+}
+
+// Scans all requests.  s_first [B + 1]: first tile (ATOMS: first row pair)
+// of every request; CTA 0 leaves the plan and its totals in the workspace.
+// A request whose tiles (ATOMS: row pairs or work) pass what the host's
+// bounds gave room for is refused.
+template <bool ATOMS>
+__device__ void make_plan(const ChunkParams& p, bool leader, int32_t* s_first, int64_t* s_warp) {
+  const int64_t cap = ATOMS ? p.cap_pairs : p.cap_tiles;
+  int64_t first = 0, work = 0;
+  __shared__ unsigned long long s_used, s_work;   // what the accepted requests take
+  if (threadIdx.x == 0) {
+    s_first[0] = 0;
+    s_used = s_work = 0ull;
+  }
+  __syncthreads();
+  for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    unsigned err = 0;
+    ReqPlan r = {};
+    if (b < p.B) r = check_request(p, b, &err);
+    const int64_t units = ATOMS ? (int64_t)r.npair * p.Hkv : r.ntiles;
+    int64_t tot_u, tot_w = 0;
+    const int64_t upto = first + block_scan64(units, s_warp, &tot_u);
+    const int64_t mine = ATOMS ? units * (r.len - r.lo) : 0;
+    const int64_t done = ATOMS ? work + block_scan64(r.n > 0 ? mine : 0, s_warp, &tot_w) : 0;
+    if (b < p.B) {
+      // once over, the sums stay over: every later request with units is
+      // refused too, and the totals end with the last accepted one
+      if (units > 0 && (upto > cap || (ATOMS && done > p.cap_work))) {
+        err = SDK_ERR_CAPACITY;
+        r.n = 0;
+      } else if (leader && units > 0) {
+        atomicMax(&s_used, (unsigned long long)upto);
+        atomicMax(&s_work, (unsigned long long)done);
+      }
+      s_first[b + 1] = (int)min(upto, cap);
+      if (leader) {
+        r.tile0 = (int)min(upto - units, cap);
+        r.pair0 = r.tile0;
+        r.work0 = min(done - mine, (int64_t)p.cap_work);
+        if (r.n == 0) r.ntiles = r.npair = 0;
+        p.plan[b] = r;
+        if (err) record_error(p.hdr, err, 0x75000000u | (uint32_t)b);
+      }
+    }
+    first += tot_u;
+    work += tot_w;
+  }
+  __syncthreads();
+  if (leader && threadIdx.x == 0) {
+    // p.plan[B]: the totals
+    ReqPlan t = {};
+    t.pair0 = t.tile0 = (int)s_used;
+    t.work0 = (int64_t)s_work;
+    p.plan[p.B] = t;
+  }
+}
+
+// The last b in [0, B) with first[b] <= e.
+__device__ __forceinline__ int find_first(const int32_t* first, int B, int e) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= e) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The request whose rows hold row `tok` of q (one of them; the caller checks).
+__device__ __forceinline__ int find_request(const ChunkParams& p, int tok) {
+  return find_first(p.cu_q, p.B, tok);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^e for a row of bf16 bits with largest magnitude mx (as bits) so that its
+// largest entry's exponent becomes `to` (e = 0 for a row of zeros, or one
+// with infinities or NaN, which spoil that row alone), as two factors that
+// are each in float's range.
+__device__ __forceinline__ void row_scale(uint32_t mx, int to, float* a, float* b) {
+  int e = (mx >> 7) == 255u || mx == 0u ? 0 : to + 127 - (int)max(mx >> 7, 1u);
+  *a = __uint_as_float((uint32_t)(min(e, 126) + 127) << 23);
+  *b = __uint_as_float((uint32_t)(max(e - 126, 0) + 127) << 23);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+}  // namespace sdk

@@ -32,13 +32,15 @@ struct StoreParams {
 
 // One request of a chunk call, as every kernel of the call sees it.
 struct ReqPlan {
-  int row0;     // first row of q
-  int n;        // new tokens (0: idle or refused)
-  int len;      // tokens in the store
-  int lo;       // first token any row sees, rounded down to a tile
-  int tile0;    // its first tile in the workspace
+  int row0;       // first row of q
+  int n;          // new tokens (0: idle or refused)
+  int len;        // tokens in the store
+  int lo;         // first token any row sees, rounded down to a tile
+  int tile0;      // its first tile in the workspace
   int ntiles;
-  int pad[2];
+  int pair0;      // its first pair of packed rows
+  int npair;      // pairs per KV head
+  int64_t work0;  // (pair, token) units before it
 };
 
 struct ChunkParams {
@@ -52,20 +54,36 @@ struct ChunkParams {
   uint16_t* out;
   float* lse;
   WsHeader* hdr;
-  ReqPlan* plan;
-  __half* kt;            // rebuilt key tiles [tile][Hkv][tile image]
+  ReqPlan* plan;         // [B + 1], the last one the totals
+  // by tiles: rebuilt key and value tiles [tile][Hkv][tile image], partial
+  // sums of the splits [split][row][..]
+  __half* kt;
   __half* vt;
-  float2* part_ml;       // partial sums of the splits [split][row][..]
+  float2* part_ml;
   float* part_o;
-  int64_t n_tok;
-  int B, Hq, Hkv, g, d, n, n_pages, page_size, max_pages;
+  // by atoms: <q, D_K> of row pairs [pair][n_pad], the rows' scales, scores
+  // of (pair, token), and the weights per atom as operand images
+  __half2* qd;
+  float* row_scale;
+  float2* score;
+  char* wimg;
+  int64_t n_tok, cap_pairs, cap_work;
+  int B, Hq, Hkv, g, d, n, n_pad, n_pages, page_size, max_pages;
   int max_q, max_len, window, causal, cap_tiles, mblocks, splits;
+  int ctas, ksplits, row_tiles;
   float scale;
 };
 
 sdk_status launch_block_tables(const TableParams& p, cudaStream_t stream);
 sdk_status launch_paged_store(const StoreParams& p, cudaStream_t stream);
-sdk_status launch_chunk_attn(ChunkParams p, char* workspace, cudaStream_t stream);
+// total_len as the caller's (0: B * max_len)
+sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
+                             cudaStream_t stream);
+// the two forms' parts (chunk_attn.cu, chunk_atoms.cu)
+size_t atoms_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
+                             int max_len, int64_t total_len);
+sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
+                              cudaStream_t stream, bool* taken);
 // total bytes of the chunk attention's workspace
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len);

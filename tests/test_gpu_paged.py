@@ -336,6 +336,10 @@ SHAPES = [
     dict(lens=[2100, 1900, 35], new=[1, 2, 1], Hq=8, Hkv=2, n=32768), # few rows, several splits
     dict(lens=[1500], new=[700], Hq=16, Hkv=1, P=128),                # g = 16
     dict(lens=[4096], new=[2], Hq=64, Hkv=1, d=64, n=1001),           # g = 64, odd atom count
+    dict(lens=[9000], new=[1], Hq=32, Hkv=8, n=32768, P=64),          # few rows, long contexts:
+    dict(lens=[20001, 0, 500, 1], new=[3, 0, 2, 1], Hq=12, Hkv=4, n=1001, P=24, d=64),
+    dict(lens=[70000, 3], new=[1, 1], Hq=1, Hkv=1, n=32767, P=7),     # one row of a pair
+    dict(lens=[1100] * 30, new=[1] * 30, Hq=4, Hkv=2, n=513, d=64),   # many requests
 ]
 
 
@@ -369,7 +373,8 @@ def test_rows_behind_the_last_request_stay():
     assert torch.equal(got[:21], c.run()) and (got[21:] == 3.0).all() and (lse[21:] == 5.0).all()
 
 
-@pytest.mark.parametrize("lens,new", [([400], [300]), ([3000], [2]), ([260, 50], [1, 50])])
+@pytest.mark.parametrize("lens,new", [([400], [300]), ([3000], [2]), ([260, 50], [1, 50]),
+                                      ([40000, 50], [3, 1])])
 def test_bad_words_in_masked_places(lens, new):
     """NaN and infinite coefficients and atoms past the dictionary in tokens
     that only the last row sees: recorded, every other row is as before."""
@@ -388,16 +393,61 @@ def test_bad_words_in_masked_places(lens, new):
         assert torch.equal(got[keep], want[keep])
 
 
-def test_bad_query_rows_stay_alone():
-    c = Case([500, 900], [140, 1], seed=6)
+@pytest.mark.parametrize("lens,new,i", [([500, 900], [140, 1], 70), ([40000, 900], [3, 1], 1)])
+def test_bad_query_rows_stay_alone(lens, new, i):
+    c = Case(lens, new, seed=6)
     want = c.run()
-    c.q[3, 2] = float("nan")
-    c.q[70, 5, 7] = float("inf")
+    c.q[2, 2] = float("nan")
+    c.q[i, 5, 7] = float("inf")
     got = c.run()
     bad = torch.zeros(got.shape[:2], dtype=torch.bool, device="cuda")
-    bad[3, 2] = bad[70, 5] = True
+    bad[2, 2] = bad[i, 5] = True
     assert torch.equal(got[~bad], want[~bad])
-    assert torch.isnan(got[3, 2]).all() and torch.isnan(got[70, 5]).all()
+    assert torch.isnan(got[2, 2]).all() and torch.isnan(got[i, 5]).all()
+
+
+def test_few_rows_refusals():
+    """Refusals and bad pages on the long-context form.  (Refusing a request
+    cuts the others' contexts at other places: equal within the tolerance.)"""
+    c = Case([50000, 30000], [2, 1], Hkv=2, Hq=4, seed=7)
+    T, Hq, d = c.q.shape
+    ref, tol, _, _ = _attend_ref(c.q, c.dk, c.dv, c.pages, c.table, c.lens, c.cu, True, 0,
+                                 1 / math.sqrt(d))
+    near = lambda out, rows: ((out.double() - ref).abs() <= tol)[rows].all()
+    ws = c.workspace()
+
+    def go(status, kept, left, **kw):
+        out = torch.full_like(c.q, 9.0)
+        c.run(ws=ws, out=out, **kw)
+        assert _status(ws)[0] == status and near(out, kept) and (out[left] == 9.0).all()
+
+    a, b = slice(0, 2), slice(2, 3)
+    go(3, b, a, max_len=40000)
+    # room for 2 pairs (two tokens, two heads a group) x 2 KV heads x 50000
+    # tokens: request 0 takes it all
+    go(3, a, b, total=50000)
+    c.lens = [50000, -4]
+    go(6, a, b, total=80000)
+    c.lens = [50000, 30000]
+    want = c.run()
+    c.table[0, 7] = -1
+    out = c.run(ws=ws)
+    assert _status(ws)[0] == 6 and torch.equal(out[b], want[b])
+
+
+@pytest.mark.parametrize("size", [1e-5, 1.0, 3e3])
+def test_few_rows_value_sizes(size):
+    """Value coefficients of any size, and one token a thousand times the
+    others (the fixed point of the weights follows the sums)."""
+    c = Case([40000], [1], Hq=4, Hkv=2, n=5000, seed=11)
+    w = c.pages[:, :, :, 1]
+    coef = (w >> 16).to(torch.int16).view(torch.float16).float() * size
+    coef[5, :, 3] *= 1000.0 if size < 100 else 10.0
+    coef = coef.clamp(-65504, 65504)           # as words are made (include/sdk.h)
+    good = (w & 0x7FFF) < 5000
+    c.pages[:, :, :, 1] = torch.where(
+        good, (coef.half().view(torch.int16).to(torch.int32) << 16) | (w & 0x7FFF), w)
+    c.check()
 
 
 def test_refused_requests():
