@@ -83,8 +83,10 @@ struct QdCfg {
   static constexpr int kOffBar = kOffB + kN * D * 2;
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffRow = kOffMisc + 16;         // [kN] largest |q| of a column's row
-  static constexpr int kOffScan = kOffRow + kN * 4;     // [32] int64, then first pairs [B + 1]
+  static constexpr int kOffMax = kOffMisc + 16;         // [kN] largest |q| of a column's row
+  static constexpr int kOffRow = kOffMax + kN * 4;      // [kN] its row of q, -1: none
+  static constexpr int kOffUp = kOffRow + kN * 4;       // [kN] its scale
+  static constexpr int kOffScan = kOffUp + kN * 4;      // [32] int64, then first pairs [B + 1]
   static constexpr int kSmem = kOffScan + 256 + (SDK_MAX_REQUESTS + 1) * 4 + 1024;
   static_assert(kSmem <= 232448, "exceeds the 227 KB shared memory of one sm_100 CTA");
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |
@@ -105,7 +107,9 @@ __global__ void __launch_bounds__(192, 1)
   uint8_t* smem = tc::align_smem_1k(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  uint32_t* s_max = reinterpret_cast<uint32_t*>(smem + C::kOffRow);
+  uint32_t* s_max = reinterpret_cast<uint32_t*>(smem + C::kOffMax);
+  int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kOffRow);
+  float* s_up = reinterpret_cast<float*>(smem + C::kOffUp);
   int64_t* s_warp = reinterpret_cast<int64_t*>(smem + C::kOffScan);
   int32_t* s_pair0 = reinterpret_cast<int32_t*>(smem + C::kOffScan + 256);
   volatile uint32_t* s_abort = misc;
@@ -138,40 +142,64 @@ __global__ void __launch_bounds__(192, 1)
   const int pair_base = blockIdx.y * (kN / 2);
 
   // the tile's query rows as the K-major B operand (zero past the last)
-  for (int e = tid; e < kN * (D / 8); e += 192) {
-    const int col = e / (D / 8), kc = e % (D / 8);
-    const int pair = pair_base + col / 2;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < kN) {
+    const int pair = pair_base + tid / 2;
+    int row = -1;
     if (pair < n_pairs) {
       const int b = find_first(s_pair0, p.B, pair);
       const int row0 = p.cu_q[b], n = p.cu_q[b + 1] - row0;
       const int npair = (int)(((int64_t)n * p.g + 1) / 2);
       const int rel = pair - s_pair0[b], h = rel / npair;
-      const int r = (rel - h * npair) * 2 + (col & 1);
+      const int r = (rel - h * npair) * 2 + (tid & 1);
       if (r < n * p.g) {
         const int i = r / p.g;
-        const int64_t row = (int64_t)(row0 + i) * p.Hq + h * p.g + (r - i * p.g);
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + row * D) + kc);
+        row = (row0 + i) * p.Hq + h * p.g + (r - i * p.g);
       }
-      uint32_t mx = 0u;
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) mx = max(mx, max(x[u] & 0x7FFFu, (x[u] >> 16) & 0x7FFFu));
-      if (mx) atomicMax(&s_max[col], mx);
     }
-    *reinterpret_cast<uint4*>(smem + C::kOffB + (kc >> 3) * (kN * 128) + col * 128 +
-                              (((kc & 7) ^ (col & 7)) << 4)) = v;
+    s_row[tid] = row;
+  }
+  __syncthreads();
+  {
+    constexpr int kBatch = 4;    // loads in flight
+    for (int e0 = tid; e0 < kN * (D / 8); e0 += kBatch * 192) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int e = e0 + u * 192, row = e < kN * (D / 8) ? s_row[e / (D / 8)] : -1;
+        v[u] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                       : __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)row * D) + e % (D / 8));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int e = e0 + u * 192;
+        if (e >= kN * (D / 8)) break;
+        const int col = e / (D / 8), kc = e % (D / 8);
+        uint32_t mx = 0u;
+        const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = max(mx, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+        if (mx) atomicMax(&s_max[col], mx);
+        *reinterpret_cast<uint4*>(smem + C::kOffB + (kc >> 3) * (kN * 128) + col * 128 +
+                                  (((kc & 7) ^ (col & 7)) << 4)) = v[u];
+      }
+    }
   }
   tc::fence_proxy_async();
+  __syncthreads();
+  if (tid < kN) {
+    // one factor does: where it is short of the row's scale (entries below
+    // 2^-126) the scores vanish anyway
+    float up, rest;
+    row_scale(s_max[tid], 0, &up, &rest);
+    s_up[tid] = up;
+    if (blockIdx.x == 0 && pair_base + tid / 2 < n_pairs)
+      p.row_scale[2 * pair_base + tid] = p.scale * 1.44269504f / up;
+  }
+  tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *s_tmem;
   if (pair_base < n_pairs) {   // else nothing but the totals
-    if (blockIdx.x == 0 && tid < kN && pair_base + tid / 2 < n_pairs) {
-      float a, b;
-      row_scale(s_max[tid], 0, &a, &b);
-      p.row_scale[2 * pair_base + tid] = p.scale * 1.44269504f / a / b;
-    }
     if (warp == 0) {
       if (lane == 0) {
         bool ok = true;
@@ -253,18 +281,15 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               if (cb + c >= live) break;
-              float x[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                float f, f2;
-                row_scale(s_max[cb + c + u], 0, &f, &f2);
-                x[u] = __uint_as_float(v[c + u]) * f * f2;
-                if (fabsf(x[u]) > 65504.0f && !isinf(x[u])) {
-                  over = true;
-                  x[u] = copysignf(65504.0f, x[u]);
-                }
+              const float2 up = *reinterpret_cast<const float2*>(s_up + cb + c);
+              float x0 = __uint_as_float(v[c]) * up.x, x1 = __uint_as_float(v[c + 1]) * up.y;
+              if (fmaxf(fabsf(x0), fabsf(x1)) > 65504.0f) {
+                // infinities come from the query and stay
+                over |= (fabsf(x0) > 65504.0f && !isinf(x0)) || (fabsf(x1) > 65504.0f && !isinf(x1));
+                if (!isinf(x0)) x0 = fminf(fmaxf(x0, -65504.0f), x0 != x0 ? x0 : 65504.0f);
+                if (!isinf(x1)) x1 = fminf(fmaxf(x1, -65504.0f), x1 != x1 ? x1 : 65504.0f);
               }
-              dst[(int64_t)(c / 2) * p.n_pad] = __floats2half2_rn(x[0], x[1]);
+              dst[(int64_t)(c / 2) * p.n_pad] = __floats2half2_rn(x0, x1);
             }
           }
         }
@@ -287,6 +312,8 @@ __global__ void __launch_bounds__(192, 1)
 
 namespace {
 
+constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
+
 // A token's position in the pages, stepped by kTokThreads without division.
 struct PageAt {
   int col, off;
@@ -303,6 +330,29 @@ struct PageAt {
     }
   }
 };
+
+// Index of the 128-byte record at `at` for KV head h (all of them fit in 32
+// bits: 2^32 records are 512 GB), kNoRecord where not wanted or on a page
+// outside the pool.
+__device__ __forceinline__ uint32_t record_of(const ChunkParams& p, const int32_t* table,
+                                              const PageAt& at, int h, bool wanted, int b) {
+  if (!wanted) return kNoRecord;
+  const int page = table[at.col];
+  if (page < 0 || page >= p.n_pages) {
+    record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
+    return kNoRecord;
+  }
+  return ((uint32_t)page * (uint32_t)p.Hkv + (uint32_t)h) * (uint32_t)p.page_size + (uint32_t)at.off;
+}
+
+// The lane's four words of the record that lane (l & ~3) | k holds; v: the
+// value half.
+__device__ __forceinline__ uint4 load_words(const ChunkParams& p, uint32_t rec, int k, int v) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t r = __shfl_sync(0xffffffffu, rec, (lane & ~3) | k);
+  if (r == kNoRecord) return make_uint4(0u, 0u, 0u, 0u);
+  return __ldg(reinterpret_cast<const uint4*>(p.pages) + (int64_t)r * 8 + v * 4 + (lane & 3));
+}
 
 template <typename T, typename F>
 __device__ __forceinline__ T block_reduce(T v, T* s_red, F f) {
@@ -348,7 +398,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
   __shared__ float s_red[32];
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ uint32_t s_abort;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int own = (lane >> 2) + 8 * (lane & 3), mine = warp * 32 + own;
   const int P = p.page_size;
   const int dcol = kTokThreads / P, doff = kTokThreads - dcol * P;
   const int64_t W = p.plan[p.B].work0;
@@ -416,57 +467,78 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
       return;
     }
 
-    // ---- scores
+    // ---- scores.  A warp takes 32 tokens at a time; four lanes read one
+    // token's record (64 contiguous bytes), lane l ends with the sums of
+    // token own(l) = l / 4 + 8 (l % 4).
     float m0 = -INFINITY, m1 = -INFINITY;
     bool nan0 = false, nan1 = false;
     uint32_t top = 0u;                        // largest atom index met
     PageAt at;
-    at.init(min(ta + tid, rp.len), P);
-    for (int t = ta + tid; t < tb; t += kTokThreads, at.step(dcol, doff, P)) {
-      const int page = table[at.col];
-      float a0 = 0.0f, a1 = 0.0f;
-      if (page >= 0 && page < p.n_pages) {
-        const uint4* rec = reinterpret_cast<const uint4*>(
-            p.pages + (((int64_t)page * p.Hkv + h) * P + at.off) * 2 * kAtoms);
-        uint4 x[4];
+    at.init(min(ta + mine, rp.len), P);
+    for (int u = warp * 32; u < cnt; u += kTokThreads, at.step(dcol, doff, P)) {
+      const int t = ta + u + own;
+      const uint32_t rec = record_of(p, table, at, h, t < tb, b);
+      uint4 x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = __ldg(rec + k);
+      for (int k = 0; k < 4; ++k) x[k] = load_words(p, rec, k, 0);
+      float a[4][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        a[k][0] = a[k][1] = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a = word_idx(ws[i]);
-            const float2 qd = __half22float2(*reinterpret_cast<const __half2*>(tab + a));
-            const float c = word_coef(ws[i]);
-            a0 = fmaf(c, qd.x, a0);
-            a1 = fmaf(c, qd.y, a1);
-            if (!FULL) top = max(top, a);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at_ = word_idx(ws[i]);
+          const float2 qd = __half22float2(*reinterpret_cast<const __half2*>(tab + at_));
+          const float c = word_coef(ws[i]);
+          a[k][0] = fmaf(c, qd.x, a[k][0]);
+          a[k][1] = fmaf(c, qd.y, a[k][1]);
+          if (!FULL) top = max(top, at_);
         }
-        if (!(fabsf(a0) < INFINITY) || !(fabsf(a1) < INFINITY)) {
-          // a bad word, or a bad query row: the words are made harmless
-          bool bad = false;
-          a0 = a1 = 0.0f;
-          for (int k = 0; k < kAtoms; ++k) {
-            const uint32_t y =
-                clean_word(__ldg(reinterpret_cast<const uint32_t*>(rec) + k), &bad);
-            const float2 qd = __half22float2(*reinterpret_cast<const __half2*>(tab + word_idx(y)));
-            a0 = fmaf(word_coef(y), qd.x, a0);
-            a1 = fmaf(word_coef(y), qd.y, a1);
+      }
+      // sum over the four lanes, each keeping one token: first tokens k and
+      // k ^ 1 change lanes, then k and k ^ 2
+      float a0, a1;
+      {
+        const bool odd = lane & 1, high = lane & 2;
+        float s[2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            const float give = odd ? a[2 * kk][e] : a[2 * kk + 1][e];
+            const float keep = odd ? a[2 * kk + 1][e] : a[2 * kk][e];
+            s[kk][e] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
           }
+        a0 = (high ? s[1][0] : s[0][0]) +
+             __shfl_xor_sync(0xffffffffu, high ? s[0][0] : s[1][0], 2);
+        a1 = (high ? s[1][1] : s[0][1]) +
+             __shfl_xor_sync(0xffffffffu, high ? s[0][1] : s[1][1], 2);
+      }
+      if (t < tb) {
+        if (rec != kNoRecord && (!(fabsf(a0) < INFINITY) || !(fabsf(a1) < INFINITY))) {
+          // a bad word, or a bad query row: the words are made harmless
+          const uint32_t* words = p.pages + (int64_t)rec * 2 * kAtoms;
+          bool bad = false;
+          float b0 = 0.0f, b1 = 0.0f;
+          for (int k = 0; k < kAtoms; ++k) {
+            const uint32_t y = clean_word(__ldg(words + k), &bad);
+            const float2 qd = __half22float2(*reinterpret_cast<const __half2*>(tab + word_idx(y)));
+            b0 = fmaf(word_coef(y), qd.x, b0);
+            b1 = fmaf(word_coef(y), qd.y, b1);
+          }
+          if (!(fabsf(a0) < INFINITY)) a0 = b0;
+          if (!(fabsf(a1) < INFINITY)) a1 = b1;
           if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
         }
-      } else {
-        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
+        a0 = t >= see0[0] && t <= see1[0] ? a0 * sc0 : -INFINITY;
+        a1 = t >= see0[1] && t <= see1[1] ? a1 * sc1 : -INFINITY;
+        nan0 |= a0 != a0;
+        nan1 |= a1 != a1;
+        m0 = fmaxf(m0, a0);
+        m1 = fmaxf(m1, a1);
+        score[t - ta] = make_float2(a0, a1);
       }
-      a0 = t >= see0[0] && t <= see1[0] ? a0 * sc0 : -INFINITY;
-      a1 = t >= see0[1] && t <= see1[1] ? a1 * sc1 : -INFINITY;
-      nan0 |= a0 != a0;
-      nan1 |= a1 != a1;
-      m0 = fmaxf(m0, a0);
-      m1 = fmaxf(m1, a1);
-      score[t - ta] = make_float2(a0, a1);
     }
     if (!FULL && top >= (uint32_t)p.n)
       record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
@@ -492,15 +564,14 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
       // the size of p c from one token per thread; only tokens that the row
       // sees have a say in its rounding
       float sa = 0.0f, sp = 0.0f, spa = 0.0f;
-      at.init(min(ta + tid, rp.len), P);
-      if (tid < cnt) {
-        const float2 s2 = score[tid];
+      at.init(min(ta + mine, rp.len), P);
+      if (mine < cnt) {
+        const float2 s2 = score[mine];
         sp = ex2((e ? s2.y : s2.x) - m);
-        const int page = table[at.col];
-        if (sp > 0.0f && page >= 0 && page < p.n_pages) {
-          const uint32_t* rec =
-              p.pages + ((((int64_t)page * p.Hkv + h) * P + at.off) * 2 + 1) * kAtoms;
-          for (int k = 0; k < kAtoms; ++k) sa += fabsf(word_coef(rec[k]));
+        const uint32_t rec = record_of(p, table, at, h, sp > 0.0f, b);
+        if (rec != kNoRecord) {
+          const uint32_t* words = p.pages + (int64_t)rec * 2 * kAtoms + kAtoms;
+          for (int k = 0; k < kAtoms; ++k) sa += fabsf(word_coef(words[k]));
           spa = sp * sa;
         }
       }
@@ -526,37 +597,38 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
         __syncthreads();
         float za = 0.0f, aa = 0.0f;
         uint32_t vtop = 0u;
-        at.init(min(ta + tid, rp.len), P);
-        for (int t = ta + tid; t < tb; t += kTokThreads, at.step(dcol, doff, P)) {
-          const float2 s2 = score[t - ta];
-          const float pr = ex2((e ? s2.y : s2.x) - m);
+        at.init(min(ta + mine, rp.len), P);
+        for (int u = warp * 32; u < cnt; u += kTokThreads, at.step(dcol, doff, P)) {
+          const int t = ta + u + own;
+          float pr = 0.0f;
+          if (t < tb) {
+            const float2 s2 = score[t - ta];
+            pr = ex2((e ? s2.y : s2.x) - m);
+          }
           za += pr;
-          const int page = table[at.col];
-          if (!(pr > 0.0f) || page < 0 || page >= p.n_pages) continue;
-          const uint4* rec = reinterpret_cast<const uint4*>(
-              p.pages + ((((int64_t)page * p.Hkv + h) * P + at.off) * 2 + 1) * kAtoms);
+          const uint32_t rec = record_of(p, table, at, h, pr > 0.0f, b);
           uint4 x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = __ldg(rec + k);
-          const float pu = pr * up;
-          float ca = 0.0f;
-          bool bad = false;
+          for (int k = 0; k < 4; ++k) x[k] = load_words(p, rec, k, 1);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
+            const float pk = __shfl_sync(0xffffffffu, pr, (lane & ~3) | k);
+            const float pu = pk * up;
             uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float ca = 0.0f;
+            bool bad = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (clean) ws[i] = clean_word(ws[i], &bad);
-              const uint32_t a = word_idx(ws[i]);
+              const uint32_t at_ = word_idx(ws[i]);
               const float c = word_coef(ws[i]);
               ca += fabsf(c);
-              const int add = __float2int_rn(pu * c);
-              if (add != 0) atomicAdd(reinterpret_cast<int*>(tab) + a, add);
-              if (!FULL) vtop = max(vtop, a);
+              atomicAdd(reinterpret_cast<int*>(tab) + at_, __float2int_rn(pu * c));
+              if (!FULL) vtop = max(vtop, at_);
             }
+            aa = fmaf(pk, ca, aa);
+            if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
           }
-          aa = fmaf(pr, ca, aa);
-          if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
         }
         if (!FULL && vtop >= (uint32_t)p.n)
           record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
@@ -742,12 +814,16 @@ __global__ void __launch_bounds__(128, 1)
   }
 }
 
-// The sums of a row's segments over all atom ranges; a thread per dim.
+// The sums of a row's segments over all atom ranges, a block per row: a
+// thread per dim and group of partial sums, the groups joined in order.
+// Latency-bound: the loads of a thread are independent and in flight
+// together.
 template <int D>
-__global__ void __launch_bounds__(128) atoms_join_kernel(ChunkParams p) {
-  const int64_t row = (int64_t)blockIdx.x * (128 / D) + threadIdx.x / D;
-  const int dim = threadIdx.x % D;
-  if (row >= p.n_tok * p.Hq) return;
+__global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
+  constexpr int G = 1024 / D;
+  __shared__ float s_o[1024];
+  const int64_t row = blockIdx.x;
+  const int dim = threadIdx.x % D, grp = threadIdx.x / D;
   const int tok = (int)(row / p.Hq), hq = (int)(row - (int64_t)tok * p.Hq);
   const ReqPlan rp = p.plan[find_request(p, tok)];
   // rows of no request, or of a refused one, stay as they were
@@ -755,32 +831,38 @@ __global__ void __launch_bounds__(128) atoms_join_kernel(ChunkParams p) {
   const int h = hq / p.g, r = (tok - rp.row0) * p.g + (hq - h * p.g);
   const int64_t q = (int64_t)h * rp.npair + (r >> 1), span = rp.len - rp.lo;
   const int64_t w0 = rp.work0 + q * span, w1 = w0 + span, W = p.plan[p.B].work0;
-  const int pair = rp.pair0 + (int)q;
   float m = -INFINITY, z = 0.0f, o = 0.0f;
   if (span > 0) {
+    // the CTAs whose shares meet [w0, w1)
     int c0 = (int)((double)w0 / (double)W * p.ctas);
     c0 = min(max(c0, 0), p.ctas - 1);
     while (c0 > 0 && W * c0 / p.ctas > w0) --c0;
     while (c0 + 1 < p.ctas && W * (c0 + 1) / p.ctas <= w0) ++c0;
+    int c1 = c0 + 1;
+    while (c1 < p.ctas && W * c1 / p.ctas < w1) ++c1;
     const int64_t rows = (int64_t)p.row_tiles * kN;
-    for (int pass = 0; pass < 2; ++pass)
-      for (int c = c0; c < p.ctas; ++c) {
-        const int64_t a = max(w0, W * c / p.ctas), e = min(w1, W * (c + 1) / p.ctas);
-        if (W * c / p.ctas >= w1) break;
-        if (a >= e) continue;
-        const int64_t i = 2 * (int64_t)(c + pair) + (r & 1);
-        const float2 ml = p.part_ml[i];
-        if (pass == 0) {
-          m = fmaxf(m, ml.x);
-        } else if (!(ml.x == -INFINITY && ml.y == 0.0f)) {   // else it saw nothing
-          const float f = ex2(ml.x - m);
-          z = fmaf(ml.y, f, z);
-          float s = 0.0f;
-          for (int k = 0; k < p.ksplits; ++k) s += p.part_o[(k * rows + i) * D + dim];
-          o = fmaf(s, f, o);
-        }
-      }
+    const int64_t first = 2 * (int64_t)(rp.pair0 + q) + (r & 1);
+    for (int c = c0; c < c1; ++c)
+      if (W * c / p.ctas < W * (c + 1) / p.ctas) m = fmaxf(m, p.part_ml[first + 2 * c].x);
+    for (int c = c0; c < c1; ++c) {
+      if (W * c / p.ctas == W * (c + 1) / p.ctas) continue;
+      const int64_t i = first + 2 * c;
+      const float2 ml = p.part_ml[i];
+      if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // it saw nothing
+      const float f = ex2(ml.x - m);
+      z = fmaf(ml.y, f, z);
+      const float* src = p.part_o + i * D + dim;
+      float s = 0.0f;
+#pragma unroll 8
+      for (int k = grp; k < p.ksplits; k += G) s += src[k * rows * D];
+      o = fmaf(s, f, o);
+    }
   }
+  s_o[threadIdx.x] = o;
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int k = 1; k < G; ++k) o += s_o[k * D + dim];
   const bool any = z > 0.0f || z != z;
   p.out[row * D + dim] =
       __bfloat16_as_ushort(__float2bfloat16_rn(z != z ? z : any ? o / z : 0.0f));
@@ -821,8 +903,7 @@ static sdk_status launch_atoms_d(const CUtensorMap& kmap, const CUtensorMap& vma
     atoms_token_kernel<false><<<p.ctas, kTokThreads, kTab * 4, stream>>>(p);
   atoms_out_kernel<D><<<dim3((unsigned)p.ksplits, (unsigned)p.row_tiles), 128, OutCfg::kSmem,
                         stream>>>(vmap, p);
-  const int64_t per = 128 / D;
-  atoms_join_kernel<D><<<(unsigned)((p.n_tok * p.Hq + per - 1) / per), 128, 0, stream>>>(p);
+  atoms_join_kernel<D><<<(unsigned)(p.n_tok * p.Hq), 1024, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SDK_OK : SDK_ERR_CUDA;
 }
 
