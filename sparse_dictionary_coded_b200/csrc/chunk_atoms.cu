@@ -21,7 +21,8 @@ constexpr int kN = 128;            // rows per MMA tile
 constexpr int kM = 128;            // atoms per QD tile, head dims of w D_V
 constexpr int kChunk = 64;         // atoms per step of w D_V
 constexpr int kTab = SDK_MAX_ATOMS;
-constexpr int kTokThreads = 1024;
+constexpr int kMaxCtas = 512;      // CTAs of the token kernel
+constexpr int kTokThreads = 768;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -42,8 +43,9 @@ AtomCut atom_cut(int B, int64_t n_tok, int Hq, int Hkv, int n, int max_q, int ma
   if (total_len > 0 && total_len < tokens) tokens = total_len;
   c.work = tokens * Hkv * each;
   // a share below a thousand tokens would leave threads idle
-  const int64_t want = c.work / kTokThreads;
-  c.ctas = (int)(want < 1 ? 1 : want > num_sms() ? num_sms() : want);
+  const int64_t want = c.work / 1024;
+  const int most = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+  c.ctas = (int)(want < 1 ? 1 : want > most ? most : want);
   // a segment is a CTA's share of one pair: at most ctas + pairs of them
   c.row_tiles = (int)((2 * (c.ctas + c.pairs) + kN - 1) / kN);
   c.chunks = (n + kChunk - 1) / kChunk;
@@ -137,6 +139,18 @@ __global__ void __launch_bounds__(192, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // the first dictionary tiles are on their way while the plan is made
+  auto load_tile = [&](int k) {
+    const int st = k % C::kStages, a = blockIdx.x + k * gridDim.x;
+    tc::mbar_expect_tx(bar_full(st), (uint32_t)C::kStageB);
+#pragma unroll
+    for (int kb = 0; kb < D / 64; ++kb)
+      tc::tma_load_2d(s0 + st * C::kStageB + kb * (kM * 128), &kmap, kb * 64, a * kM, bar_full(st));
+  };
+  const int my_tiles = (n_tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int early = min(my_tiles, C::kStages);
+  if (tid == 0)
+    for (int k = 0; k < early; ++k) load_tile(k);
   make_plan<true>(p, blockIdx.x == 0 && blockIdx.y == 0, s_pair0, s_warp);
   const int n_pairs = s_pair0[p.B];
   const int pair_base = blockIdx.y * (kN / 2);
@@ -203,18 +217,14 @@ __global__ void __launch_bounds__(192, 1)
     if (warp == 0) {
       if (lane == 0) {
         bool ok = true;
-        int k = 0;
-        for (int a = blockIdx.x; a < n_tiles; a += gridDim.x, ++k) {
+        int k = early;
+        for (; k < my_tiles; ++k) {
           const int st = k % C::kStages;
           if (!tc::mbar_wait(bar_empty(st), ((uint32_t)(k / C::kStages) & 1u) ^ 1u, s_abort)) {
             ok = false;
             break;
           }
-          tc::mbar_expect_tx(bar_full(st), (uint32_t)C::kStageB);
-#pragma unroll
-          for (int kb = 0; kb < D / 64; ++kb)
-            tc::tma_load_2d(s0 + st * C::kStageB + kb * (kM * 128), &kmap, kb * 64, a * kM,
-                            bar_full(st));
+          load_tile(k);
         }
         if (!ok) {
           if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x60000000u | blockIdx.x);
@@ -300,6 +310,11 @@ __global__ void __launch_bounds__(192, 1)
       }
     }
   }
+  if (pair_base >= n_pairs && tid == 0)   // no rows here: the early copies land all the same
+    for (int k = 0; k < early; ++k) {
+      uint32_t never = 0u;
+      tc::mbar_wait(bar_full(k), 0u, &never, 100000000ull);
+    }
   __syncthreads();
   if (warp == 1) {
     tc::tc_fence_after();
@@ -331,18 +346,23 @@ struct PageAt {
   }
 };
 
-// Index of the 128-byte record at `at` for KV head h (all of them fit in 32
-// bits: 2^32 records are 512 GB), kNoRecord where not wanted or on a page
-// outside the pool.
-__device__ __forceinline__ uint32_t record_of(const ChunkParams& p, const int32_t* table,
-                                              const PageAt& at, int h, bool wanted, int b) {
+// The page at `at`, -1 where not wanted; looked up two steps before its
+// records are read.
+__device__ __forceinline__ int page_of(const int32_t* table, const PageAt& at, bool wanted) {
+  return wanted ? table[at.col] : -1;
+}
+
+// Index of the 128-byte record at offset `off` of a page for KV head h (all
+// of them fit in 32 bits: 2^32 records are 512 GB), kNoRecord where not
+// wanted or on a page outside the pool.
+__device__ __forceinline__ uint32_t record_of(const ChunkParams& p, int page, int off, int h,
+                                              bool wanted, int b) {
   if (!wanted) return kNoRecord;
-  const int page = table[at.col];
   if (page < 0 || page >= p.n_pages) {
     record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
     return kNoRecord;
   }
-  return ((uint32_t)page * (uint32_t)p.Hkv + (uint32_t)h) * (uint32_t)p.page_size + (uint32_t)at.off;
+  return ((uint32_t)page * (uint32_t)p.Hkv + (uint32_t)h) * (uint32_t)p.page_size + (uint32_t)off;
 }
 
 // The lane's four words of the record that lane (l & ~3) | k holds; v: the
@@ -354,14 +374,14 @@ __device__ __forceinline__ uint4 load_words(const ChunkParams& p, uint32_t rec, 
   return __ldg(reinterpret_cast<const uint4*>(p.pages) + (int64_t)r * 8 + v * 4 + (lane & 3));
 }
 
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, T* s_red, F f) {
+template <typename F>
+__device__ __forceinline__ float block_reduce(float v, float zero, float* s_red, F f) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = s_red[threadIdx.x & 31];
+  v = (threadIdx.x & 31) < kTokThreads / 32 ? s_red[threadIdx.x & 31] : zero;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
@@ -373,6 +393,75 @@ __device__ __forceinline__ uint32_t clean_word(uint32_t w, bool* bad) {
   *bad = true;
   if (w & 0x03FF0000u) return w & 0x7FFFu;
   return (w & 0x80007FFFu) | 0x7BFF0000u;
+}
+
+// Adds p c of the segment's tokens [ta, ta + cnt) to the table for row e of
+// the pair, with m the row's maximum and `up` the fixed point.  Returns this
+// thread's part of sum_t p_t and of sum_t p_t sum_j |c_tj|.  CLEAN: bad words
+// are made harmless and recorded.  Tokens of no weight are not read.
+template <bool FULL, bool CLEAN>
+__device__ __forceinline__ float2 add_weights(const ChunkParams& p, uint32_t* tab,
+                                              const float2* score, const int32_t* table, int h,
+                                              int ta, int cnt, int e, float m, float up, int len,
+                                              int b) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int own = (lane >> 2) + 8 * (lane & 3), mine = warp * 32 + own;
+  const int P = p.page_size, dcol = kTokThreads / P, doff = kTokThreads - dcol * P;
+  float z = 0.0f, sum = 0.0f;
+  uint32_t top = 0u;
+  auto score_of = [&](int u) {
+    if (u >= cnt) return -INFINITY;
+    const float2 s = score[u];
+    return e ? s.y : s.x;
+  };
+  // words one step ahead, scores and pages two
+  PageAt at;
+  at.init(min(ta + mine, len), P);
+  uint4 x[4], y[4];
+  float w0 = ex2(score_of(mine) - m), s1 = score_of(mine + kTokThreads);
+  const int pg0 = page_of(table, at, mine < cnt);
+  const uint32_t rec0 = record_of(p, pg0, at.off, h, w0 > 0.0f, b);
+  at.step(dcol, doff, P);
+  int pg1 = page_of(table, at, mine + kTokThreads < cnt), off1 = at.off;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = load_words(p, rec0, k, 1);
+#pragma unroll 1
+  for (int u = warp * 32; u < cnt; u += kTokThreads) {
+    const float w1 = ex2(s1 - m);
+    const uint32_t rec1 = record_of(p, pg1, off1, h, w1 > 0.0f, b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = load_words(p, rec1, k, 1);
+    at.step(dcol, doff, P);
+    s1 = score_of(u + own + 2 * kTokThreads);
+    pg1 = page_of(table, at, u + own + 2 * kTokThreads < cnt);
+    off1 = at.off;
+    z += w0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float pk = __shfl_sync(0xffffffffu, w0, (lane & ~3) | k);
+      const float pu = pk * up;
+      uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      float ca = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (CLEAN) ws[i] = clean_word(ws[i], &bad);
+        const uint32_t a = word_idx(ws[i]);
+        const float c = word_coef(ws[i]);
+        ca += fabsf(c);
+        atomicAdd(reinterpret_cast<int*>(tab) + a, __float2int_rn(pu * c));
+        if (!FULL) top = max(top, a);
+      }
+      sum = fmaf(pk, ca, sum);
+      if (CLEAN && bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = y[k];
+    w0 = w1;
+  }
+  if (!FULL && top >= (uint32_t)p.n)
+    record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
+  return make_float2(z, sum);
 }
 
 }  // namespace
@@ -473,14 +562,24 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
     float m0 = -INFINITY, m1 = -INFINITY;
     bool nan0 = false, nan1 = false;
     uint32_t top = 0u;                        // largest atom index met
+    // words one step ahead, pages two
     PageAt at;
     at.init(min(ta + mine, rp.len), P);
-    for (int u = warp * 32; u < cnt; u += kTokThreads, at.step(dcol, doff, P)) {
-      const int t = ta + u + own;
-      const uint32_t rec = record_of(p, table, at, h, t < tb, b);
-      uint4 x[4];
+    uint4 x[4], y[4];
+    uint32_t rec = record_of(p, page_of(table, at, mine < cnt), at.off, h, mine < cnt, b);
+    at.step(dcol, doff, P);
+    int pg1 = page_of(table, at, mine + kTokThreads < cnt), off1 = at.off;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = load_words(p, rec, k, 0);
+    for (int k = 0; k < 4; ++k) x[k] = load_words(p, rec, k, 0);
+#pragma unroll 1
+    for (int u = warp * 32; u < cnt; u += kTokThreads) {
+      const int t = ta + u + own;
+      const uint32_t rec1 = record_of(p, pg1, off1, h, t + kTokThreads < tb, b);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = load_words(p, rec1, k, 0);
+      at.step(dcol, doff, P);
+      pg1 = page_of(table, at, t + 2 * kTokThreads < tb);
+      off1 = at.off;
       float a[4][2];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -539,12 +638,15 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
         m1 = fmaxf(m1, a1);
         score[t - ta] = make_float2(a0, a1);
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = y[k];
+      rec = rec1;
     }
     if (!FULL && top >= (uint32_t)p.n)
       record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
     const bool row_nan0 = __syncthreads_or(nan0) != 0, row_nan1 = __syncthreads_or(nan1) != 0;
-    m0 = block_reduce(m0, s_red, fmax2);
-    m1 = block_reduce(m1, s_red, fmax2);
+    m0 = block_reduce(m0, -INFINITY, s_red, fmax2);
+    m1 = block_reduce(m1, -INFINITY, s_red, fmax2);
 
     // ---- weights, row by row
 #pragma unroll 1
@@ -568,7 +670,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
       if (mine < cnt) {
         const float2 s2 = score[mine];
         sp = ex2((e ? s2.y : s2.x) - m);
-        const uint32_t rec = record_of(p, table, at, h, sp > 0.0f, b);
+        const uint32_t rec = record_of(p, page_of(table, at, true), at.off, h, sp > 0.0f, b);
         if (rec != kNoRecord) {
           const uint32_t* words = p.pages + (int64_t)rec * 2 * kAtoms + kAtoms;
           for (int k = 0; k < kAtoms; ++k) sa += fabsf(word_coef(words[k]));
@@ -576,9 +678,9 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
         }
       }
       const float seen = (float)max(1, __syncthreads_count(sp > 0.0f));
-      sa = block_reduce(sa, s_red, fadd2);
-      sp = block_reduce(sp, s_red, fadd2);
-      spa = block_reduce(spa, s_red, fadd2);
+      sa = block_reduce(sa, 0.0f, s_red, fadd2);
+      sp = block_reduce(sp, 0.0f, s_red, fadd2);
+      spa = block_reduce(spa, 0.0f, s_red, fadd2);
       float bound = 8.0f * fmaxf(sa / seen, fmaxf(spa, sp * (sa / seen)) / (float)min(cnt, kTokThreads) *
                                                 (float)cnt);
       float z = 0.0f, inv = 0.0f;
@@ -595,45 +697,14 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
         for (int a = tid; a < kTab / 4; a += kTokThreads)
           reinterpret_cast<uint4*>(tab)[a] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        float za = 0.0f, aa = 0.0f;
-        uint32_t vtop = 0u;
-        at.init(min(ta + mine, rp.len), P);
-        for (int u = warp * 32; u < cnt; u += kTokThreads, at.step(dcol, doff, P)) {
-          const int t = ta + u + own;
-          float pr = 0.0f;
-          if (t < tb) {
-            const float2 s2 = score[t - ta];
-            pr = ex2((e ? s2.y : s2.x) - m);
-          }
-          za += pr;
-          const uint32_t rec = record_of(p, table, at, h, pr > 0.0f, b);
-          uint4 x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = load_words(p, rec, k, 1);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float pk = __shfl_sync(0xffffffffu, pr, (lane & ~3) | k);
-            const float pu = pk * up;
-            uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            float ca = 0.0f;
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (clean) ws[i] = clean_word(ws[i], &bad);
-              const uint32_t at_ = word_idx(ws[i]);
-              const float c = word_coef(ws[i]);
-              ca += fabsf(c);
-              atomicAdd(reinterpret_cast<int*>(tab) + at_, __float2int_rn(pu * c));
-              if (!FULL) vtop = max(vtop, at_);
-            }
-            aa = fmaf(pk, ca, aa);
-            if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
-          }
-        }
-        if (!FULL && vtop >= (uint32_t)p.n)
-          record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
-        z = block_reduce(za, s_red, fadd2);
-        aa = block_reduce(aa, s_red, fadd2);
+        float za, aa;
+        const float2 sums =
+            clean ? add_weights<FULL, true>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b)
+                  : add_weights<FULL, false>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b);
+        za = sums.x;
+        aa = sums.y;
+        z = block_reduce(za, 0.0f, s_red, fadd2);
+        aa = block_reduce(aa, 0.0f, s_red, fadd2);
         if (aa * up < 2.0e9f) break;          // every sum fits (false for NaN)
         if (!(aa < INFINITY)) {
           clean = true;
@@ -822,6 +893,7 @@ template <int D>
 __global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
   constexpr int G = 1024 / D;
   __shared__ float s_o[1024];
+  __shared__ float2 s_ml[kMaxCtas];
   const int64_t row = blockIdx.x;
   const int dim = threadIdx.x % D, grp = threadIdx.x / D;
   const int tok = (int)(row / p.Hq), hq = (int)(row - (int64_t)tok * p.Hq);
@@ -842,20 +914,27 @@ __global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
     while (c1 < p.ctas && W * c1 / p.ctas < w1) ++c1;
     const int64_t rows = (int64_t)p.row_tiles * kN;
     const int64_t first = 2 * (int64_t)(rp.pair0 + q) + (r & 1);
-    for (int c = c0; c < c1; ++c)
-      if (W * c / p.ctas < W * (c + 1) / p.ctas) m = fmaxf(m, p.part_ml[first + 2 * c].x);
-    for (int c = c0; c < c1; ++c) {
-      if (W * c / p.ctas == W * (c + 1) / p.ctas) continue;
-      const int64_t i = first + 2 * c;
-      const float2 ml = p.part_ml[i];
-      if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // it saw nothing
-      const float f = ex2(ml.x - m);
-      z = fmaf(ml.y, f, z);
-      const float* src = p.part_o + i * D + dim;
-      float s = 0.0f;
+    const int segs = c1 - c0;
+    for (int c = threadIdx.x; c < segs; c += 1024)   // an empty share has no sums
+      s_ml[c] = W * (c0 + c) / p.ctas < W * (c0 + c + 1) / p.ctas
+                    ? p.part_ml[first + 2 * (c0 + c)]
+                    : make_float2(-INFINITY, 0.0f);
+    __syncthreads();
+    for (int c = 0; c < segs; ++c) m = fmaxf(m, s_ml[c].x);
+    for (int c = 0; c < segs; ++c)
+      if (s_ml[c].y != 0.0f) z = fmaf(s_ml[c].y, ex2(s_ml[c].x - m), z);
+    __syncthreads();
+    for (int c = threadIdx.x; c < segs; c += 1024)
+      s_ml[c].y = s_ml[c].y != 0.0f ? ex2(s_ml[c].x - m) : 0.0f;
+    __syncthreads();
+    const float* src = p.part_o + (first + 2 * (int64_t)c0) * D + dim;
+    const int all = segs * p.ksplits;
 #pragma unroll 8
-      for (int k = grp; k < p.ksplits; k += G) s += src[k * rows * D];
-      o = fmaf(s, f, o);
+    for (int i = grp; i < all; i += G) {
+      const int c = i / p.ksplits, k = i - c * p.ksplits;
+      const float f = s_ml[c].y;
+      // what saw nothing has no sums to read
+      o = fmaf(f, f != 0.0f ? src[(k * rows + 2 * c) * D] : 0.0f, o);
     }
   }
   s_o[threadIdx.x] = o;
