@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t bar_done = bar(2 * C::kStages + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_tiles = (p.n + kM - 1) / kM;
+  pdl_launch();
   if (tid == 0) {
     *s_abort = 0u;
     for (int i = 0; i < C::kNumBars; ++i)
@@ -491,6 +492,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
   const int own = (lane >> 2) + 8 * (lane & 3), mine = warp * 32 + own;
   const int P = p.page_size;
   const int dcol = kTokThreads / P, doff = kTokThreads - dcol * P;
+  pdl_launch();
+  pdl_wait();
   const int64_t W = p.plan[p.B].work0;
   int64_t w = W * blockIdx.x / gridDim.x;
   const int64_t w_end = W * (blockIdx.x + 1) / gridDim.x;
@@ -778,6 +781,8 @@ __global__ void __launch_bounds__(128, 1)
   auto bar_empty = [&](int s) { return tc::smem_u32(&bars[C::kStages + s]); };
   const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages]);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch();
+  pdl_wait();
   // rows that no segment wrote are not read
   const int rows = 2 * (p.ctas + p.plan[p.B].pair0);
   if ((int)blockIdx.y * kN >= rows) return;
@@ -885,17 +890,18 @@ __global__ void __launch_bounds__(128, 1)
   }
 }
 
-// The sums of a row's segments over all atom ranges, a block per row: a
-// thread per dim and group of partial sums, the groups joined in order.
-// Latency-bound: the loads of a thread are independent and in flight
-// together.
+// The sums of a row's segments over all atom ranges: a block takes 32 dims
+// of a row, a thread per dim and group of partial sums, the groups joined in
+// order.  Latency-bound: the loads of a thread are independent and in
+// flight together.
 template <int D>
-__global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
-  constexpr int G = 1024 / D;
-  __shared__ float s_o[1024];
+__global__ void __launch_bounds__(512) atoms_join_kernel(ChunkParams p) {
+  constexpr int G = 16;
+  __shared__ float s_o[512];
   __shared__ float2 s_ml[kMaxCtas];
-  const int64_t row = blockIdx.x;
-  const int dim = threadIdx.x % D, grp = threadIdx.x / D;
+  pdl_wait();
+  const int64_t row = blockIdx.x / (D / 32);
+  const int dim = (blockIdx.x % (D / 32)) * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
   const int tok = (int)(row / p.Hq), hq = (int)(row - (int64_t)tok * p.Hq);
   const ReqPlan rp = p.plan[find_request(p, tok)];
   // rows of no request, or of a refused one, stay as they were
@@ -915,7 +921,7 @@ __global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
     const int64_t rows = (int64_t)p.row_tiles * kN;
     const int64_t first = 2 * (int64_t)(rp.pair0 + q) + (r & 1);
     const int segs = c1 - c0;
-    for (int c = threadIdx.x; c < segs; c += 1024)   // an empty share has no sums
+    for (int c = threadIdx.x; c < segs; c += 512)   // an empty share has no sums
       s_ml[c] = W * (c0 + c) / p.ctas < W * (c0 + c + 1) / p.ctas
                     ? p.part_ml[first + 2 * (c0 + c)]
                     : make_float2(-INFINITY, 0.0f);
@@ -924,7 +930,7 @@ __global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
     for (int c = 0; c < segs; ++c)
       if (s_ml[c].y != 0.0f) z = fmaf(s_ml[c].y, ex2(s_ml[c].x - m), z);
     __syncthreads();
-    for (int c = threadIdx.x; c < segs; c += 1024)
+    for (int c = threadIdx.x; c < segs; c += 512)
       s_ml[c].y = s_ml[c].y != 0.0f ? ex2(s_ml[c].x - m) : 0.0f;
     __syncthreads();
     const float* src = p.part_o + (first + 2 * (int64_t)c0) * D + dim;
@@ -941,7 +947,7 @@ __global__ void __launch_bounds__(1024) atoms_join_kernel(ChunkParams p) {
   __syncthreads();
   if (grp > 0) return;
 #pragma unroll
-  for (int k = 1; k < G; ++k) o += s_o[k * D + dim];
+  for (int k = 1; k < G; ++k) o += s_o[k * 32 + threadIdx.x];
   const bool any = z > 0.0f || z != z;
   p.out[row * D + dim] =
       __bfloat16_as_ushort(__float2bfloat16_rn(z != z ? z : any ? o / z : 0.0f));
@@ -976,14 +982,15 @@ static sdk_status launch_atoms_d(const CUtensorMap& kmap, const CUtensorMap& vma
   unsigned gx = (unsigned)num_sms() / ty;
   gx = gx < 1 ? 1 : gx > (unsigned)tiles ? (unsigned)tiles : gx;
   atoms_qd_kernel<D><<<dim3(gx, ty), 192, QdCfg<D>::kSmem, stream>>>(kmap, p);
-  if (p.n == kTab)
-    atoms_token_kernel<true><<<p.ctas, kTokThreads, kTab * 4, stream>>>(p);
-  else
-    atoms_token_kernel<false><<<p.ctas, kTokThreads, kTab * 4, stream>>>(p);
-  atoms_out_kernel<D><<<dim3((unsigned)p.ksplits, (unsigned)p.row_tiles), 128, OutCfg::kSmem,
-                        stream>>>(vmap, p);
-  atoms_join_kernel<D><<<(unsigned)(p.n_tok * p.Hq), 1024, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SDK_OK : SDK_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
+  const auto token = p.n == kTab ? atoms_token_kernel<true> : atoms_token_kernel<false>;
+  if (launch_after(token, dim3((unsigned)p.ctas), kTokThreads, kTab * 4, stream, p) != cudaSuccess ||
+      launch_after(atoms_out_kernel<D>, dim3((unsigned)p.ksplits, (unsigned)p.row_tiles), 128,
+                   OutCfg::kSmem, stream, vmap, p) != cudaSuccess ||
+      launch_after(atoms_join_kernel<D>, dim3((unsigned)(p.n_tok * p.Hq * (D / 32))), 512, 0,
+                   stream, p) != cudaSuccess)
+    return SDK_ERR_CUDA;
+  return SDK_OK;
 }
 
 sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,

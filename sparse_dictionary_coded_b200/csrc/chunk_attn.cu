@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
   int32_t* s_tile0 = sm;              // [B + 1]
   __shared__ int64_t s_warp[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch();
   make_plan<false>(p, blockIdx.x == 0, s_tile0, s_warp);
 
   constexpr int LPR = D / 8;           // lanes per record
@@ -224,6 +225,8 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   using C = ACfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const int g = p.g;
+  pdl_launch();
+  pdl_wait();
   // the work item: consecutive CTAs share a KV head's tiles
   int w = blockIdx.x;
   const int split = w % p.splits;
@@ -548,6 +551,7 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
   constexpr int E = D / 32;
+  pdl_wait();
   const int64_t R = p.n_tok * p.Hq;
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -648,12 +652,12 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
   const int64_t ctas = (int64_t)p.B * p.Hkv * p.mblocks * p.splits;
   if (ctas > 0x7FFFFFFF) return SDK_ERR_INVALID_ARG;
-  chunk_attn_kernel<D><<<(unsigned)ctas, kAThreads, ACfg<D>::kSmem, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
-  if (p.splits > 1) {
-    chunk_join_kernel<D><<<(unsigned)((p.n_tok * p.Hq + 7) / 8), 256, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
-  }
+  if (launch_after(chunk_attn_kernel<D>, dim3((unsigned)ctas), kAThreads, ACfg<D>::kSmem, stream,
+                   p) != cudaSuccess)
+    return SDK_ERR_CUDA;
+  if (p.splits > 1 && launch_after(chunk_join_kernel<D>, dim3((unsigned)((p.n_tok * p.Hq + 7) / 8)),
+                                   256, 0, stream, p) != cudaSuccess)
+    return SDK_ERR_CUDA;
   return SDK_OK;
 }
 
