@@ -12,7 +12,6 @@ namespace sdk {
 namespace {
 
 constexpr int kRebThreads = 256;
-constexpr int kRebTok = 32;       // tokens of one work item of rebuild_kernel
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -45,12 +44,14 @@ __device__ __forceinline__ int tile_off(int r, int c8) {
 
 // The plan of the call and the rebuilt tiles.  Every CTA makes the plan
 // itself (a scan over the requests' tile counts); CTA 0 leaves it in the
-// workspace for the attention kernel.  A work item is 32 tokens of one KV
-// head; D / 8 lanes rebuild one vector (16-byte pieces of an atom's row), a
-// warp a token's key and value (two tokens at head_dim 64).  Bound by the
-// gathers of 2 x 16 atom rows (8 KB per token and head at head_dim 128)
-// from L2.
-template <int D>
+// workspace for the attention kernel.  D / 8 lanes rebuild one vector
+// (16-byte pieces of an atom's row), a warp a token's key and value (two
+// tokens at head_dim 64), TOK tokens one after the other with their code
+// words read up front.  Bound by the gathers of 2 x 16 atom rows (8 KB per
+// token and head at head_dim 128) from L2: 2.1 GB at 10.7 TB/s for 32768
+// tokens of 8 heads.  With few tokens it is the chain of loads that counts,
+// so there a warp takes one (TOK 1: 20.6 -> 11 us for eight short chats).
+template <int D, int TOK>
 __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
   extern __shared__ int32_t sm[];
   int32_t* s_tile0 = sm;              // [B + 1]
@@ -62,15 +63,15 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
   constexpr int LPR = D / 8;           // lanes per record
   constexpr int TPS = 32 / (2 * LPR);  // tokens a warp rebuilds at a time
   constexpr int WPL = 16 / LPR;        // code words a lane holds
-  constexpr int kTokWarp = kRebTok / (kRebThreads / 32);
+  constexpr int kItemTok = TOK * TPS * (kRebThreads / 32);   // tokens of a work item
   const int rec = lane / LPR, sub = lane % LPR;
   const int kv = rec & 1;
   const uint4* dict = reinterpret_cast<const uint4*>(kv ? p.dv : p.dk);
   char* tiles = reinterpret_cast<char*>(kv ? p.vt : p.kt);
-  const int64_t items = (int64_t)s_tile0[p.B] * p.Hkv * (kTile / kRebTok);
+  const int64_t items = (int64_t)s_tile0[p.B] * p.Hkv * (kTile / kItemTok);
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int part = (int)(it % (kTile / kRebTok));
-    const int64_t th = it / (kTile / kRebTok);
+    const int part = (int)(it % (kTile / kItemTok));
+    const int64_t th = it / (kTile / kItemTok);
     const int h = (int)(th % p.Hkv);
     const int tile = (int)(th / p.Hkv);
     const int b = find_first(s_tile0, p.B, tile);
@@ -79,46 +80,60 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
     const int t_tile = rq.lo + (tile - s_tile0[b]) * kTile;
     const int t_end = rq.n > 0 ? rq.len : 0;
     char* dst = tiles + ((int64_t)tile * p.Hkv + h) * (kTile * D * 2);
-#pragma unroll 1
-    for (int u = 0; u < kTokWarp; u += TPS) {
-      const int r = part * kRebTok + warp * kTokWarp + u + (rec >> 1);   // row of the tile
-      const int t = t_tile + r;
-      uint32_t w[WPL];
+    const int r0 = part * kItemTok + warp * (TOK * TPS) + (rec >> 1);   // row of the tile
+    uint32_t w[TOK][WPL];
+    int page[TOK];
 #pragma unroll
-      for (int i = 0; i < WPL; ++i) w[i] = 0u;
-      if (t < t_end) {
-        const int col = t / p.page_size, off = t - col * p.page_size;
-        const int page = p.table[(int64_t)b * p.max_pages + col];
-        if (page >= 0 && page < p.n_pages) {
-          const uint32_t* src =
-              p.pages + ((((int64_t)page * p.Hkv + h) * p.page_size + off) * 2 + kv) * kAtoms;
+    for (int u = 0; u < TOK; ++u) {
+      const int t = t_tile + r0 + u * TPS;
+      page[u] = t < t_end ? p.table[(int64_t)b * p.max_pages + t / p.page_size] : -1;
+    }
 #pragma unroll
-          for (int i = 0; i < WPL; ++i) w[i] = src[sub * WPL + i];
-        } else if (sub == 0) {
-          record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
-        }
+    for (int u = 0; u < TOK; ++u) {
+      const int t = t_tile + r0 + u * TPS;
+#pragma unroll
+      for (int i = 0; i < WPL; ++i) w[u][i] = 0u;
+      if (page[u] >= 0 && page[u] < p.n_pages) {
+        const int off = t - t / p.page_size * p.page_size;
+        const uint32_t* src =
+            p.pages + ((((int64_t)page[u] * p.Hkv + h) * p.page_size + off) * 2 + kv) * kAtoms;
+#pragma unroll
+        for (int i = 0; i < WPL; ++i) w[u][i] = src[sub * WPL + i];
+      } else if (t < t_end && sub == 0) {
+        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) {
+      const int r = r0 + u * TPS;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool bad = false;
+      if (t_tile + r - (rec >> 1) < t_end) {   // the warp's first token of the step
+        uint4 v[kAtoms];
+        float c[kAtoms];
 #pragma unroll
-      for (int j = 0; j < kAtoms; ++j) {
-        const uint32_t x = __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL);
-        uint32_t a = word_idx(x);
-        float c = word_coef(x);
-        if (a >= (uint32_t)p.n) {
-          bad = true;
-          a = 0;
-          c = 0.0f;
+        for (int j = 0; j < kAtoms; ++j) {
+          const uint32_t x = __shfl_sync(0xffffffffu, w[u][j % WPL], rec * LPR + j / WPL);
+          uint32_t a = word_idx(x);
+          c[j] = word_coef(x);
+          if (a >= (uint32_t)p.n) {
+            bad = true;
+            a = 0;
+            c[j] = 0.0f;
+          }
+          v[j] = __ldg(dict + (int64_t)a * LPR + sub);
         }
-        const uint4 v = __ldg(dict + (int64_t)a * LPR + sub);
-        acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
-        acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
-        acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
-        acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
-        acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
-        acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
-        acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
-        acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
+#pragma unroll
+        for (int j = 0; j < kAtoms; ++j) {
+          acc[0] = fmaf(c[j], bf16_lo(v[j].x), acc[0]);
+          acc[1] = fmaf(c[j], bf16_hi(v[j].x), acc[1]);
+          acc[2] = fmaf(c[j], bf16_lo(v[j].y), acc[2]);
+          acc[3] = fmaf(c[j], bf16_hi(v[j].y), acc[3]);
+          acc[4] = fmaf(c[j], bf16_lo(v[j].z), acc[4]);
+          acc[5] = fmaf(c[j], bf16_hi(v[j].z), acc[5]);
+          acc[6] = fmaf(c[j], bf16_lo(v[j].w), acc[6]);
+          acc[7] = fmaf(c[j], bf16_hi(v[j].w), acc[7]);
+        }
       }
       // fp16 tiles: 11 significand bits (bf16 would have 8, and its
       // rounding of K, V and the probabilities would double the output's
@@ -166,13 +181,14 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
 // partial sums are joined by chunk_join_kernel.
 namespace {
 
-constexpr int kAThreads = 384;     // two warpgroups of rows, one of MMA and copy warps
+constexpr int kAThreads = 384;     // a warpgroup for each row tile, one of MMA and copy warps
 // registers a thread after the split: 256 x 224 + 128 x 56 = 384 x 168, what
-// the block is launched with (the rows' 128 scores stay in registers)
+// the block is launched with (a row's 128 scores stay in registers)
 constexpr int kRegsLaunch = 168, kRegsRows = 224, kRegsRest = 56;
 static_assert(256 * kRegsRows + 128 * kRegsRest == kAThreads * kRegsLaunch, "register split");
 constexpr float kPUp = 7.0f;       // log2 of P's offset
 constexpr float kSlack = 8.0f;     // log2 of how far a tile may exceed m
+constexpr int kPolyOf = 4;         // every 4th pair of exponentials on the FMA units
 
 template <int D>
 struct ACfg {
@@ -180,8 +196,9 @@ struct ACfg {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kOffQ = kStages * kTileB;
   static constexpr int kOffBar = kOffQ + 2 * kTileB;
-  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2;
-  static constexpr int kSmem = kOffBar + kNumBars * 8 + 64 + 1024;   // + alignment slack
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;       // + alignment slack
   static_assert(kSmem <= 232448, "exceeds the 227 KB shared memory of one sm_100 CTA");
   // D f32, A and B f16; S: both K-major, N = 128; O: B MN-major, N = D
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) |
@@ -190,18 +207,73 @@ struct ACfg {
                                       ((uint32_t)(kTile >> 4) << 24);
 };
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  const uint32_t z = 0u;
+// The MMAs' operands by the low halves of their descriptors (tc::smem_desc,
+// tc::smem_desc_mn: address and leading offset; the high half is the same for
+// all tiles), so that the one issuing thread spends an addition on each.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
+  return (addr >> 4) | ((uint32_t)(kTile * 128 >> 4) << 16);
+}
+// The whole warp runs the issuing loop, so that its values stay in uniform
+// registers (which the instruction takes its operands from), and the elected
+// lane issues four steps of 16 at a time: with one lane in a branch of its
+// own the issue was the bound (2048 tokens over 32768: 1084 us, so 916 us).
+// ss: A and B 16 elements (32 bytes) further along K each step; ts: A 8 TMEM
+// columns, B 16 rows of 128 bytes.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(z), "r"(z), "r"(z), "r"(z)
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+      "mov.b64 da, {a, %4};\n\tmov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\t"
+      "mov.b64 da, {a, %4};\n\tmov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, t;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\t"
+      "mov.b64 da, {a, %4};\n\tmov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, t;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\t"
+      "mov.b64 da, {a, %4};\n\tmov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, t;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+      "mov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\t"
+      "mov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\t"
+      "mov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\t"
+      "mov.b64 db, {b, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, t;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 
-// 32 lanes x 32 bits, 32 consecutive columns per thread.
+// 32 lanes x 32 bits, 32 and 16 consecutive columns per thread.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -214,11 +286,72 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[30]), "r"(v[31]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+// Two floats in a register pair, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x of two values, x <= 15, on the FMA units: x = n + f with n the nearest
+// integer (left in the low bits by adding 1.5 * 2^23), 2^f by a polynomial of
+// degree 3 fitted to the relative error on [-1/2, 1/2] with value 1 at 0
+// (at most 2^-13.2, a fifth of the fp16 rounding that follows), n added to
+// the exponent.  Below -127 the result is 0.
+__device__ __forceinline__ void ex2_fma(uint64_t x2, float* y0, float* y1) {
+  const float kBig = 12582912.0f;
+  float a, b;
+  unpack2(x2, &a, &b);
+  x2 = pack2(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
+  const uint64_t t = add2(x2, pack2(kBig, kBig));
+  const uint64_t n = add2(t, pack2(-kBig, -kBig));
+  const uint64_t f = fma2(n, pack2(-1.0f, -1.0f), x2);
+  uint64_t q = fma2(f, pack2(0.05500885908f, 0.05500885908f), pack2(0.2422110112f, 0.2422110112f));
+  q = fma2(q, f, pack2(0.6932829447f, 0.6932829447f));
+  q = fma2(q, f, pack2(1.0f, 1.0f));
+  float t0, t1, q0, q1;
+  unpack2(t, &t0, &t1);
+  unpack2(q, &q0, &q1);
+  *y0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+  *y1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 }  // namespace
+
+// A bounded wait of a whole warp, all lanes with the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          unsigned long long limit = tc::kWaitNs) {
+  if (__all_sync(0xffffffffu, tc::mbar_try(bar, parity))) return true;
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, limit));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p) {
@@ -242,16 +375,18 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
 
   uint8_t* smem = tc::align_smem_1k(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffBar + C::kNumBars * 8);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* s_abort = misc + 0;
   volatile uint32_t* s_tmem = misc + 1;
   const uint32_t s0 = tc::smem_u32(smem);
   auto bar_full = [&](int s) { return tc::smem_u32(&bars[s]); };
   auto bar_empty = [&](int s) { return tc::smem_u32(&bars[C::kStages + s]); };
   auto bar_s = [&](int i) { return tc::smem_u32(&bars[2 * C::kStages + i]); };
-  auto bar_p = [&](int i) { return tc::smem_u32(&bars[2 * C::kStages + 2 + i]); };
-  const uint32_t bar_q = tc::smem_u32(&bars[2 * C::kStages + 4]);
-  const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages + 5]);
+  auto bar_p = [&](int i, int half) {
+    return tc::smem_u32(&bars[2 * C::kStages + 2 + 2 * i + half]);
+  };
+  const uint32_t bar_q = tc::smem_u32(&bars[2 * C::kStages + 6]);
+  const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages + 7]);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // tiles the block's rows see, and this split's share of them
@@ -271,7 +406,7 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   if (tid == 0) {
     *s_abort = 0u;
     for (int s = 0; s < 2 * C::kStages + 2; ++s) tc::mbar_init(tc::smem_u32(&bars[s]), 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(bar_p(i), 4);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(bar_p(i >> 1, i & 1), 4);
     tc::mbar_init(bar_q, 4 * nact);
     tc::mbar_init(bar_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -319,55 +454,77 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
         tc::mbar_wait(bar_full(k % C::kStages), (uint32_t)(k / C::kStages) & 1u, &never, 100000000ull);
       }
     }
-    if (warp == 8 && lane == 0 && nt > 0) {
+    if (warp == 8 && nt > 0) {
     // --------------------------------------------------------------- MMAs
-      bool ok = tc::mbar_wait(bar_q, 0u, s_abort);
-      auto wait_full = [&](int k) {
-        return tc::mbar_wait(bar_full(k % C::kStages), (uint32_t)(k / C::kStages) & 1u, s_abort);
-      };
-      auto mma_s = [&](int i, int k) {
-        const uint32_t a = s0 + C::kOffQ + i * C::kTileB, bb = s0 + (k % C::kStages) * C::kTileB;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;
-          tc::tc_mma(tm_s(i), tc::smem_desc(a + o), tc::smem_desc(bb + o), C::kIdescS, ks > 0);
+      bool ok = warp_wait(bar_q, 0u, s_abort);
+      // the ring's next stage and its parity
+      int st = 0;
+      uint32_t par = 0;
+      auto next = [&]() {
+        if (++st == C::kStages) {
+          st = 0;
+          par ^= 1u;
         }
-        tc::tc_commit(bar_s(i));
       };
-      if (ok) ok = wait_full(0);
+      const uint32_t q_desc = desc_k(s0 + C::kOffQ);
+      auto mma_s = [&](int i, uint32_t kd) {
+        const uint32_t qd = q_desc + i * (C::kTileB >> 4);
+#pragma unroll
+        for (int kb = 0; kb < D / 64; ++kb)
+          mma_ss4(tm_s(i), qd + kb * (kTile * 128 >> 4), kd + kb * (kTile * 128 >> 4), C::kIdescS,
+                  kb > 0);
+        commit_elected(bar_s(i));
+      };
+      ok = ok && warp_wait(bar_full(0), 0u, s_abort);
       if (ok) {
         tc::tc_fence_after();
-        for (int i = 0; i < nact; ++i) mma_s(i, 0);
-        tc::tc_commit(bar_empty(0));
+        const uint32_t kd = desc_k(s0);
+        mma_s(0, kd);
+        if (nact > 1) mma_s(1, kd);
+        commit_elected(bar_empty(0));
       }
+      next();
       for (int j = 0; ok && j < nt; ++j) {
-        const int kv = 2 * j + 1, kk = 2 * j + 2;
-        ok = wait_full(kv) && (j + 1 == nt || wait_full(kk));
-        for (int i = 0; ok && i < nact; ++i) {
-          ok = tc::mbar_wait(bar_p(i), (uint32_t)j & 1u, s_abort);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t vb = s0 + (kv % C::kStages) * C::kTileB;
+        const bool more = j + 1 < nt;
+        const int sv = st;
+        ok = warp_wait(bar_full(sv), par, s_abort);
+        next();
+        const int sk = st;
+        if (more) {
+          ok = ok && warp_wait(bar_full(sk), par, s_abort);
+          next();
+        }
+        const uint32_t vd = desc_mn(s0 + sv * C::kTileB), kd = desc_k(s0 + sk * C::kTileB);
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_ts(tm_o(i), tm_s(i) + ks * 8, tc::smem_desc_mn(vb + ks * 2048, kTile * 128, 1024u),
-                   C::kIdescO, j > 0 || ks > 0);
-          if (j + 1 < nt)
-            mma_s(i, kk);
+        for (int i = 0; i < 2; ++i) {
+          if (i >= nact || !ok) break;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && warp_wait(bar_p(i, half), (uint32_t)j & 1u, s_abort);
+            if (!ok) break;
+            tc::tc_fence_after();
+            mma_ts4(tm_o(i), tm_s(i) + half * 32, vd + half * (64 * 128 >> 4), C::kIdescO,
+                    half > 0 ? 1u : (uint32_t)j);
+          }
+          if (!ok) break;
+          if (more)
+            mma_s(i, kd);
           else
-            tc::tc_commit(bar_s(i));   // O complete
+            commit_elected(bar_s(i));   // O complete
         }
         if (!ok) break;
-        tc::tc_commit(bar_empty(kv % C::kStages));
-        if (j + 1 < nt) tc::tc_commit(bar_empty(kk % C::kStages));
+        commit_elected(bar_empty(sv));
+        if (more) commit_elected(bar_empty(sk));
       }
       if (!ok) {
-        if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x79000000u | (blockIdx.x & 0xFFFFFFu));
+        if (lane == 0 && !*s_abort)
+          record_error(p.hdr, SDK_ERR_TIMEOUT, 0x79000000u | (blockIdx.x & 0xFFFFFFu));
+        __syncwarp();
         *s_abort = 1u;
         // what was issued ends before TMEM is freed
-        tc::tc_commit(bar_done);
+        commit_elected(bar_done);
         uint32_t never = 0u;
-        tc::mbar_wait(bar_done, 0u, &never, 100000000ull);
+        warp_wait(bar_done, 0u, &never, 100000000ull);
       }
     }
   } else {
@@ -431,19 +588,19 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
       for (int k = 0; k < 4; ++k) tc::tmem_ld32(tm_s(i) + lanes + k * 32, v[k]);
       tc::tmem_ld_wait();
       if (t0 + kTile - 1 > w_hi || t0 < w_lo) {
+        const int lim1 = see1 - t0, lim0 = see0 - t0;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            const int t = t0 + k * 32 + u;
-            if (t > see1 || t < see0) v[k][u] = 0xFF800000u;   // -inf
-          }
+          for (int u = 0; u < 32; ++u)
+            if (k * 32 + u > lim1 || k * 32 + u < lim0) v[k][u] = 0xFF800000u;   // -inf
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int u = 0; u < 32; ++u)
+      for (int u = 0; u < 32; u += 2)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[k][u]));
+        for (int k = 0; k < 4; ++k)
+          mx[k] = max3(mx[k], __uint_as_float(v[k][u]), __uint_as_float(v[k][u + 1]));
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
       if (__any_sync(0xffffffffu, mt > m + kSlack)) {
         // lane by lane, so that a row's result does not hang on its neighbours'
@@ -464,27 +621,38 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
         m = mn;
       }
       const float base = m == -INFINITY ? 0.0f : kPUp - m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t c2 = pack2(c, c), base2 = pack2(base, base);
+      uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t q2[32];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h2[16];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          const int e = 64 * k + 2 * u;
-          const float x0 = ex2(fmaf(__uint_as_float(v[e >> 5][e & 31]), c, base));
-          const float x1 = ex2(fmaf(__uint_as_float(v[e >> 5][(e & 31) + 1]), c, base));
-          sum[u & 1] += x0;
-          sum[2 + (u & 1)] += x1;
-          const __half2 hh = __floats2half2_rn(x0, x1);
-          q2[u] = *reinterpret_cast<const uint32_t*>(&hh);
+        for (int u = 0; u < 16; ++u) {
+          const uint64_t x =
+              fma2(pack2(__uint_as_float(v[k][2 * u]), __uint_as_float(v[k][2 * u + 1])), c2, base2);
+          float y0, y1;
+          if (u % kPolyOf == kPolyOf - 1) {
+            ex2_fma(x, &y0, &y1);
+          } else {
+            unpack2(x, &y0, &y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+          }
+          sum[u & 1] = add2(sum[u & 1], pack2(y0, y1));
+          const __half2 hh = __floats2half2_rn(y0, y1);
+          h2[u] = *reinterpret_cast<const uint32_t*>(&hh);
         }
-        tmem_st32(tm_s(i) + lanes + k * 32, q2);
+        tmem_st16(tm_s(i) + lanes + k * 16, h2);
+        if (k & 1) {   // 64 tokens of P are there: their product may begin
+          tmem_st_wait();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar_p(i, k >> 1));
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar_p(i));
+      float l0, l1;
+      unpack2(add2(sum[0], sum[1]), &l0, &l1);
+      l += l0 + l1;
     }
     if (nt > 0 && ok) {
       ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), (uint32_t)nt & 1u, s_abort));
@@ -646,9 +814,18 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
       return SDK_ERR_CUDA;
     device_setup_done(&attr_set);
   }
-  int64_t grid = (int64_t)p.cap_tiles * p.Hkv * (kTile / kRebTok);
-  if (grid > 8 * num_sms()) grid = 8 * num_sms();
-  rebuild_kernel<D><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
+  // a warp takes one step of tokens where that many warps are not more than
+  // the device holds at once, else four
+  constexpr int kStep = 32 / (2 * (D / 8)) * (kRebThreads / 32);   // tokens of a CTA's step
+  const int64_t steps = (int64_t)p.cap_tiles * p.Hkv * (kTile / kStep);
+  int64_t grid;
+  if (steps <= 8 * num_sms()) {
+    grid = steps;
+    rebuild_kernel<D, 1><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
+  } else {
+    grid = steps / 4 < 8 * num_sms() ? steps / 4 : 8 * num_sms();
+    rebuild_kernel<D, 4><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
+  }
   if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
   const int64_t ctas = (int64_t)p.B * p.Hkv * p.mblocks * p.splits;
   if (ctas > 0x7FFFFFFF) return SDK_ERR_INVALID_ARG;
