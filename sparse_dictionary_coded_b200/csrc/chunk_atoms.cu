@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(192, 1)
   const int early = min(my_tiles, C::kStages);
   if (tid == 0)
     for (int k = 0; k < early; ++k) load_tile(k);
-  make_plan<true>(p, blockIdx.x == 0 && blockIdx.y == 0, s_pair0, s_warp);
+  make_plan<true>(p, blockIdx.x == 0 && blockIdx.y == 0, s_pair0, nullptr, s_warp);
   const int n_pairs = s_pair0[p.B];
   const int pair_base = blockIdx.y * (kN / 2);
 

@@ -15,18 +15,35 @@ constexpr int kRebThreads = 256;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-struct ChunkLayout {
-  size_t plan, kt, vt, ml, po, total;
+// Most blocks of packed rows the requests' new tokens take (per KV head).
+int64_t cap_blocks(int B, int64_t n_tok, int g, int max_q) {
+  const int64_t each = ((int64_t)max_q * g + kRows - 1) / kRows * B, all = n_tok * g / kRows + B;
+  return each < all ? each : all;
+}
+
+// What share c of the work starts with, left for chunk_join_kernel.
+struct Cut {
+  int64_t u0;          // its first unit
+  int64_t lo, hi;      // the units of the block that unit belongs to
+  int row0, rows, mb, h;
 };
 
-ChunkLayout chunk_layout(int B, int64_t rows, int Hkv, int d, int64_t cap_tiles, int splits) {
+struct ChunkLayout {
+  size_t units, cuts, qs, qt, kt, vt, ml, po, total;
+};
+
+ChunkLayout chunk_layout(int B, int64_t blocks, int Hkv, int d, int64_t cap_tiles, int ctas,
+                         bool whole) {
   ChunkLayout l;
   const size_t tiles = (size_t)cap_tiles * Hkv * kTile * d * 2;
-  l.plan = sizeof(WsHeader);
-  l.kt = up256(l.plan + ((size_t)B + 1) * sizeof(ReqPlan));
+  l.units = up256(sizeof(WsHeader) + ((size_t)B + 1) * sizeof(ReqPlan));
+  l.cuts = up256(l.units + ((size_t)blocks + 1) * 8);
+  l.qs = up256(l.cuts + (size_t)ctas * sizeof(Cut));
+  l.qt = up256(l.qs + (size_t)blocks * Hkv * kRows * 4);
+  l.kt = l.qt + (size_t)blocks * Hkv * kRows * d * 2;
   l.vt = l.kt + tiles;
   l.ml = l.vt + tiles;
-  const size_t parts = splits > 1 ? (size_t)splits * rows : 0;
+  const size_t parts = whole ? 0 : (size_t)2 * ctas * kRows;
   l.po = up256(l.ml + parts * 8);
   l.total = up256(l.po + parts * d * 4);
   return l;
@@ -42,23 +59,164 @@ __device__ __forceinline__ int tile_off(int r, int c8) {
   return (c8 >> 3) * (kTile * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
 }
 
-// The plan of the call and the rebuilt tiles.  Every CTA makes the plan
-// itself (a scan over the requests' tile counts); CTA 0 leaves it in the
-// workspace for the attention kernel.  D / 8 lanes rebuild one vector
-// (16-byte pieces of an atom's row), a warp a token's key and value (two
-// tokens at head_dim 64), TOK tokens one after the other with their code
-// words read up front.  Bound by the gathers of 2 x 16 atom rows (8 KB per
-// token and head at head_dim 128) from L2: 2.1 GB at 10.7 TB/s for 32768
-// tokens of 8 heads.  With few tokens it is the chain of loads that counts,
-// so there a warp takes one (TOK 1: 20.6 -> 11 us for eight short chats).
+// The tiles that the rows of block mb of a request see: first and count.
+__device__ __forceinline__ void block_tiles(const ChunkParams& p, const ReqPlan& r, int mb, int* first,
+                                            int* count) {
+  const int lo_row = mb * kRows, hi_row = min(lo_row + kRows, r.n * p.g) - 1;
+  const int lo_pos = r.len - r.n + lo_row / p.g, hi_pos = r.len - r.n + hi_row / p.g;
+  const int t1 = p.causal ? min(hi_pos + 1, r.len) : r.len;
+  const int t0 = p.window > 0 ? max(0, lo_pos - p.window + 1) : 0;
+  *first = *count = 0;
+  if (t1 > t0) {
+    *first = (t0 - r.lo) / kTile;
+    *count = (t1 - r.lo + kTile - 1) / kTile - *first;
+  }
+}
+
+// Units of work of a block: its tiles, and before them what a block costs
+// besides (queries in, outputs out, a pipeline filled and drained: 12000
+// cycles against 3000 a tile); a block that sees nothing counts as one, so
+// that its rows are written.
+constexpr int kBlockCost = 4;
+__device__ __forceinline__ int block_units(int tiles) { return tiles > 0 ? tiles + kBlockCost : 1; }
+
+// One CTA: the running sum of the blocks' units over all requests, every
+// request's first one, and the number of shares: as many as CTAs, but of two
+// units at least.
+__device__ void plan_blocks(const ChunkParams& p, const int32_t* s_block, int64_t* s_warp) {
+  int64_t sum = 0, total;
+  const int blocks = s_block[p.B];
+  __syncthreads();                     // the plan is written
+  for (int m0 = 0; m0 < blocks; m0 += kRebThreads) {
+    const int m = m0 + threadIdx.x;
+    int64_t n = 0;
+    if (m < blocks) {
+      const int b = find_first(s_block, p.B, m);
+      int at, count;
+      const ReqPlan r = p.plan[b];
+      // a request that the tiles' capacity refused keeps its blocks' places
+      if (r.n > 0) block_tiles(p, r, m - s_block[b], &at, &count);
+      n = r.n > 0 ? block_units(count) : 0;
+    }
+    const int64_t upto = sum + block_scan64(n, s_warp, &total);
+    if (m < blocks) p.units[m + 1] = upto;
+    sum += total;
+  }
+  if (threadIdx.x == 0) p.units[0] = 0;
+  __syncthreads();
+  for (int b = threadIdx.x; b <= p.B; b += kRebThreads) {
+    p.plan[b].pair0 = s_block[b];
+    p.plan[b].work0 = p.units[s_block[b]] * p.Hkv;
+    if (b == p.B) {
+      const int64_t shares = (p.units[s_block[b]] * p.Hkv + 1) / 2;
+      p.plan[b].npair = (int)(shares < p.ctas ? (shares < 1 ? 1 : shares) : p.ctas);
+    }
+  }
+}
+
+constexpr int kPackSteps = 4;
+
+// The query rows as tiles of packed rows (row = token * g + head of the
+// group), fp16 scaled by a power of two that puts the row's largest entry
+// near 2^15 (exact: 8 significand bits), D / 8 lanes a row, a warp four steps
+// of rows at a time.
+template <int D>
+__device__ __forceinline__ void pack_queries(const ChunkParams& p, const int32_t* s_block,
+                                             int cta, int ctas) {
+  constexpr int kLanesRow = D / 8, kRowsStep = 32 / kLanesRow, kSteps = kPackSteps;
+  const int lane = threadIdx.x & 31, chunk = lane % kLanesRow;
+  const uint32_t rows = (uint32_t)(p.n_tok * p.Hq);          // below 2^31
+  const uint32_t items = (rows + kRowsStep * kSteps - 1) / (kRowsStep * kSteps);
+  const uint32_t warps = (uint32_t)ctas * (kRebThreads / 32);
+  for (uint32_t it = (uint32_t)cta * (kRebThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += warps) {
+    uint4 v[kSteps];
+    uint32_t row[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      row[k] = (it * kSteps + k) * kRowsStep + lane / kLanesRow;
+      v[k] = row[k] < rows ? __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)row[k] * D) + chunk)
+                           : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t mx = 0u;                // largest |q| as bf16 bits
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mx = max(mx, max(x[u] & 0x7FFFu, (x[u] >> 16) & 0x7FFFu));
+#pragma unroll
+      for (int o = kLanesRow / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (row[k] >= rows) continue;
+      float up, up2;
+      row_scale(mx, 14, &up, &up2);
+      uint32_t y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const __half2 hh = __floats2half2_rn(bf16_lo(x[u]) * up * up2, bf16_hi(x[u]) * up * up2);
+        y[u] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      const int tok = (int)(row[k] / (uint32_t)p.Hq), hq = (int)row[k] - tok * p.Hq;
+      const int b = find_request(p, tok);
+      unsigned err;
+      const ReqPlan rq = check_request(p, b, &err);
+      if (tok < rq.row0 || tok >= rq.row0 + rq.n) continue;   // a row of no request
+      const int h = hq / p.g, r = (tok - rq.row0) * p.g + (hq - h * p.g), rb = r % kRows;
+      if (s_block[b] + r / kRows >= s_block[b + 1]) continue;   // refused for want of room
+      const int64_t block = (int64_t)(s_block[b] + r / kRows) * p.Hkv + h;
+      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.qt) +
+                                (block * 2 + rb / kTile) * (kTile * D * 2) +
+                                tile_off(rb % kTile, chunk)) = make_uint4(y[0], y[1], y[2], y[3]);
+      if (chunk == 0) p.qscale[block * kRows + rb] = p.scale * 1.44269504f / up / up2;
+    }
+  }
+}
+
+// The plan of the call (CTA 0) and the query tiles.  rebuild_kernel runs
+// beside it.
+template <int D>
+__global__ void __launch_bounds__(kRebThreads) chunk_prep_kernel(ChunkParams p) {
+  extern __shared__ int32_t sm[];
+  int32_t* s_tile0 = sm;                  // [B + 1]
+  int32_t* s_block = s_tile0 + p.B + 1;   // [B + 1]
+  __shared__ int64_t s_warp[32];
+  pdl_launch();
+  make_plan<false>(p, blockIdx.x == 0, s_tile0, s_block, s_warp);
+  pack_queries<D>(p, s_block, blockIdx.x, gridDim.x);
+  if (blockIdx.x == 0) plan_blocks(p, s_block, s_warp);
+}
+
+// The rebuilt tiles.  Every CTA scans the requests' tile counts itself.  D / 8
+// lanes rebuild one vector (16-byte pieces of an atom's row), a warp a token's
+// key and value (two tokens at head_dim 64), TOK of them one after the other.
+// Bound by the gathers of 2 x 16 atom rows (8 KB per token and head at
+// head_dim 128) from L2: 2.1 GB at 10.7 TB/s for 32768 tokens of 8 heads, with
+// 32 warps an SM and about 8 rows a lane in flight (all 16 take registers that
+// leave 16 warps: 15 % slower).  With few tokens it is the chain of loads that
+// counts, so there a warp takes one and has all 16 rows in flight, and the
+// kernel also does chunk_prep_kernel's work (the plan on a CTA of its own).
 template <int D, int TOK>
-__global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
+__global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(ChunkParams p) {
   extern __shared__ int32_t sm[];
   int32_t* s_tile0 = sm;              // [B + 1]
+  int32_t* s_block = s_tile0 + p.B + 1;
   __shared__ int64_t s_warp[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
-  make_plan<false>(p, blockIdx.x == 0, s_tile0, s_warp);
+  make_plan<false>(p, TOK == 1 && blockIdx.x == 0, s_tile0, s_block, s_warp);
+  int start = (int)blockIdx.x, stride = (int)gridDim.x;
+  if (TOK == 1) {
+    if (blockIdx.x == 0 && gridDim.x > 1) {
+      plan_blocks(p, s_block, s_warp);
+      return;
+    }
+    if (gridDim.x > 1) {
+      start = blockIdx.x - 1;
+      stride = gridDim.x - 1;
+    }
+    // from the last CTA on: the first ones have most of the items
+    pack_queries<D>(p, s_block, stride - 1 - start, stride);
+    if (gridDim.x == 1) plan_blocks(p, s_block, s_warp);
+  }
 
   constexpr int LPR = D / 8;           // lanes per record
   constexpr int TPS = 32 / (2 * LPR);  // tokens a warp rebuilds at a time
@@ -69,11 +227,9 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
   const uint4* dict = reinterpret_cast<const uint4*>(kv ? p.dv : p.dk);
   char* tiles = reinterpret_cast<char*>(kv ? p.vt : p.kt);
   const int64_t items = (int64_t)s_tile0[p.B] * p.Hkv * (kTile / kItemTok);
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+  for (int64_t it = start; it < items; it += stride) {
     const int part = (int)(it % (kTile / kItemTok));
-    const int64_t th = it / (kTile / kItemTok);
-    const int h = (int)(th % p.Hkv);
-    const int tile = (int)(th / p.Hkv);
+    const int th = (int)(it / (kTile / kItemTok)), tile = th / p.Hkv, h = th - tile * p.Hkv;
     const int b = find_first(s_tile0, p.B, tile);
     unsigned err;
     const ReqPlan rq = check_request(p, b, &err);
@@ -81,58 +237,64 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
     const int t_end = rq.n > 0 ? rq.len : 0;
     char* dst = tiles + ((int64_t)tile * p.Hkv + h) * (kTile * D * 2);
     const int r0 = part * kItemTok + warp * (TOK * TPS) + (rec >> 1);   // row of the tile
-    uint32_t w[TOK][WPL];
-    int page[TOK];
-#pragma unroll
+#pragma unroll 1
     for (int u = 0; u < TOK; ++u) {
-      const int t = t_tile + r0 + u * TPS;
-      page[u] = t < t_end ? p.table[(int64_t)b * p.max_pages + t / p.page_size] : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < TOK; ++u) {
-      const int t = t_tile + r0 + u * TPS;
-#pragma unroll
-      for (int i = 0; i < WPL; ++i) w[u][i] = 0u;
-      if (page[u] >= 0 && page[u] < p.n_pages) {
-        const int off = t - t / p.page_size * p.page_size;
-        const uint32_t* src =
-            p.pages + ((((int64_t)page[u] * p.Hkv + h) * p.page_size + off) * 2 + kv) * kAtoms;
-#pragma unroll
-        for (int i = 0; i < WPL; ++i) w[u][i] = src[sub * WPL + i];
-      } else if (t < t_end && sub == 0) {
-        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
+      const int r = r0 + u * TPS, t = t_tile + r;
+      if (t - (rec >> 1) >= t_end) {   // the warp's tokens lie behind the context
+        // their scores are masked whatever the keys are; values must be finite
+        if (kv == 1)
+          *reinterpret_cast<uint4*>(dst + tile_off(r, sub)) = make_uint4(0u, 0u, 0u, 0u);
+        continue;
       }
-    }
+      uint32_t w[WPL];
 #pragma unroll
-    for (int u = 0; u < TOK; ++u) {
-      const int r = r0 + u * TPS;
+      for (int i = 0; i < WPL; ++i) w[i] = 0u;
+      if (t < t_end) {
+        const int col = t / p.page_size, off = t - col * p.page_size;
+        const int page = p.table[(int64_t)b * p.max_pages + col];
+        if (page >= 0 && page < p.n_pages) {
+          const uint32_t* src =
+              p.pages + ((((int64_t)page * p.Hkv + h) * p.page_size + off) * 2 + kv) * kAtoms;
+#pragma unroll
+          for (int i = 0; i < WPL; ++i) w[i] = src[sub * WPL + i];
+        } else if (sub == 0) {
+          record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
+        }
+      }
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool bad = false;
-      if (t_tile + r - (rec >> 1) < t_end) {   // the warp's first token of the step
-        uint4 v[kAtoms];
-        float c[kAtoms];
+      {
+        auto word = [&](int j) {
+          return __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL);
+        };
+        auto add = [&](float c, const uint4& v) {
+          acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
+          acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
+          acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
+          acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
+          acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
+          acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
+          acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
+          acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
+        };
+        auto atom = [&](uint32_t x) {
+          const uint32_t a = word_idx(x);
+          if (a >= (uint32_t)p.n) bad = true;
+          return a < (uint32_t)p.n ? a : 0u;
+        };
+        auto coef = [&](uint32_t x) { return word_idx(x) < (uint32_t)p.n ? word_coef(x) : 0.0f; };
+        if (TOK == 1) {
+          uint4 v[kAtoms];
 #pragma unroll
-        for (int j = 0; j < kAtoms; ++j) {
-          const uint32_t x = __shfl_sync(0xffffffffu, w[u][j % WPL], rec * LPR + j / WPL);
-          uint32_t a = word_idx(x);
-          c[j] = word_coef(x);
-          if (a >= (uint32_t)p.n) {
-            bad = true;
-            a = 0;
-            c[j] = 0.0f;
+          for (int j = 0; j < kAtoms; ++j) v[j] = __ldg(dict + (int64_t)atom(word(j)) * LPR + sub);
+#pragma unroll
+          for (int j = 0; j < kAtoms; ++j) add(coef(word(j)), v[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kAtoms; ++j) {
+            const uint32_t x = word(j);
+            add(coef(x), __ldg(dict + (int64_t)atom(x) * LPR + sub));
           }
-          v[j] = __ldg(dict + (int64_t)a * LPR + sub);
-        }
-#pragma unroll
-        for (int j = 0; j < kAtoms; ++j) {
-          acc[0] = fmaf(c[j], bf16_lo(v[j].x), acc[0]);
-          acc[1] = fmaf(c[j], bf16_hi(v[j].x), acc[1]);
-          acc[2] = fmaf(c[j], bf16_lo(v[j].y), acc[2]);
-          acc[3] = fmaf(c[j], bf16_hi(v[j].y), acc[3]);
-          acc[4] = fmaf(c[j], bf16_lo(v[j].z), acc[4]);
-          acc[5] = fmaf(c[j], bf16_hi(v[j].z), acc[5]);
-          acc[6] = fmaf(c[j], bf16_lo(v[j].w), acc[6]);
-          acc[7] = fmaf(c[j], bf16_hi(v[j].w), acc[7]);
         }
       }
       // fp16 tiles: 11 significand bits (bf16 would have 8, and its
@@ -156,6 +318,8 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
       *reinterpret_cast<uint4*>(dst + tile_off(r, sub)) = *reinterpret_cast<const uint4*>(o);
     }
   }
+  // done only when chunk_prep_kernel is: the next kernel waits for this one alone
+  if (TOK > 1) pdl_wait();
 }
 
 // ---------------------------------------------------------------- attention
@@ -175,16 +339,16 @@ __global__ void __launch_bounds__(kRebThreads) rebuild_kernel(ChunkParams p) {
 // rescaled in TMEM, which is rare); P is 2^7 above its nominal range, so it
 // stays below 2^15 and its smallest fp16 step is 2^-31 of the row's largest
 // term: what 2^18 tokens lose by it is below 2^-13.
-// q enters as fp16 scaled by a power of two per row (exact: 8 significand
-// bits, the row's largest entry near 2^15).
-// A context may be split over several CTAs (few rows, long contexts); their
-// partial sums are joined by chunk_join_kernel.
+// The CTAs stay, one per SM, and take equal shares of all tiles of all
+// blocks; a block that a share's end cuts leaves partial sums that
+// chunk_join_kernel joins.  (A CTA per block left the SMs idle for 13 % of
+// two rounds at 256 blocks, and long contexts of few rows on few SMs.)
 namespace {
 
 constexpr int kAThreads = 384;     // a warpgroup for each row tile, one of MMA and copy warps
-// registers a thread after the split: 256 x 224 + 128 x 56 = 384 x 168, what
+// registers a thread after the split: 256 x 216 + 128 x 72 = 384 x 168, what
 // the block is launched with (a row's 128 scores stay in registers)
-constexpr int kRegsLaunch = 168, kRegsRows = 224, kRegsRest = 56;
+constexpr int kRegsLaunch = 168, kRegsRows = 216, kRegsRest = 72;
 static_assert(256 * kRegsRows + 128 * kRegsRest == kAThreads * kRegsLaunch, "register split");
 constexpr float kPUp = 7.0f;       // log2 of P's offset
 constexpr float kSlack = 8.0f;     // log2 of how far a tile may exceed m
@@ -196,7 +360,7 @@ struct ACfg {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kOffQ = kStages * kTileB;
   static constexpr int kOffBar = kOffQ + 2 * kTileB;
-  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2;
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;       // + alignment slack
   static_assert(kSmem <= 232448, "exceeds the 227 KB shared memory of one sm_100 CTA");
@@ -353,6 +517,89 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, limit));
 }
 
+// The last i in [0, n) with at(i) <= v (at rising, at(0) <= v), by a whole
+// warp: 32 places a step, so that a few dependent loads find it.
+template <typename F>
+__device__ __forceinline__ int warp_search(int n, int64_t v, F at) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32, i = lo + lane * step;
+    const uint32_t under = __ballot_sync(0xffffffffu, lane * step < len && at(i) <= v);
+    const int k = 31 - __clz(under | 1u);
+    len = min(step, len - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+// A CTA's way through the work: all blocks of all KV heads of all requests in
+// that order, cut into equal shares of units.  Only a new request is looked
+// up, a block's tiles are computed.
+struct Walk {
+  int64_t u, end;      // next unit, end of the share
+  int b, h, mb;
+  int off;             // units of the block before u
+  int first, count;    // the block's tiles
+  ReqPlan rp;
+
+  // by whole warps
+  __device__ __forceinline__ void start(const ChunkParams& p, int64_t from, int64_t to) {
+    u = from;
+    end = to;
+    if (u >= end) return;
+    b = warp_search(p.B, u, [&](int i) { return p.plan[i].work0; });
+    rp = p.plan[b];
+    const int64_t* units = p.units + rp.pair0;
+    const int64_t base = units[0], per = units[rp.npair] - base, rel = u - rp.work0;
+    h = (int)(rel / per);
+    const int64_t at = base + rel - h * per;
+    mb = warp_search(rp.npair, at, [&](int i) { return units[i]; });
+    off = (int)(at - units[mb]);
+    block_tiles(p, rp, mb, &first, &count);
+  }
+  // block m of the call alone, for KV head hh; false: there is none
+  __device__ __forceinline__ bool whole(const ChunkParams& p, int m, int hh) {
+    if (m >= p.plan[p.B].pair0) return false;
+    b = warp_search(p.B, m, [&](int i) { return (int64_t)p.plan[i].pair0; });
+    rp = p.plan[b];
+    h = hh;
+    mb = m - rp.pair0;
+    off = 0;
+    if (mb >= rp.npair) return false;              // refused for want of room
+    block_tiles(p, rp, mb, &first, &count);
+    u = 0;
+    end = units();
+    return true;
+  }
+  __device__ __forceinline__ int units() const { return block_units(count); }   // of the block
+  // units of the segment that starts at u
+  __device__ __forceinline__ int take() const {
+    return (int)min((int64_t)(units() - off), end - u);
+  }
+  // its tiles: `at` the first, of n units
+  __device__ __forceinline__ int tiles(int n, int* at) const {
+    const int t0 = max(off - kBlockCost, 0), t1 = max(off + n - kBlockCost, 0);
+    *at = first + t0;
+    return count > 0 ? t1 - t0 : 0;
+  }
+  __device__ __forceinline__ void next(const ChunkParams& p, int taken) {
+    u += taken;
+    off = 0;
+    if (u >= end) return;
+    if (++mb == rp.npair) {
+      mb = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do ++b;
+        while (p.plan[b].npair == 0);
+        rp = p.plan[b];
+      }
+    }
+    block_tiles(p, rp, mb, &first, &count);
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p) {
   using C = ACfg<D>;
@@ -360,19 +607,19 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   const int g = p.g;
   pdl_launch();
   pdl_wait();
-  // the work item: consecutive CTAs share a KV head's tiles
-  int w = blockIdx.x;
-  const int split = w % p.splits;
-  w /= p.splits;
-  const int mb = p.mblocks - 1 - w % p.mblocks;   // the longest rows of a causal call first
-  w /= p.mblocks;
-  const int h = w % p.Hkv, b = w / p.Hkv;
-  const ReqPlan rp = p.plan[b];
-  const int rows = rp.n * g;                       // packed rows of this KV head
-  const int r_base = mb * 2 * kTile;
-  if (r_base >= rows) return;
-  const int nact = rows - r_base > kTile ? 2 : 1;  // MMA tiles with rows
-
+  int64_t u0 = 0, u1 = 0;
+  Walk walk;
+  if (p.whole) {                                   // CTA = block
+    const int m = (int)blockIdx.x / p.Hkv;
+    if (!walk.whole(p, m, (int)blockIdx.x - m * p.Hkv)) return;
+  } else {
+    const int64_t total = p.plan[p.B].work0;
+    const int shares = p.plan[p.B].npair;
+    if ((int)blockIdx.x >= shares) return;
+    u0 = total * blockIdx.x / shares;
+    u1 = total * (blockIdx.x + 1) / shares;
+    walk.start(p, u0, u1);
+  }
   uint8_t* smem = tc::align_smem_1k(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -385,29 +632,19 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   auto bar_p = [&](int i, int half) {
     return tc::smem_u32(&bars[2 * C::kStages + 2 + 2 * i + half]);
   };
-  const uint32_t bar_q = tc::smem_u32(&bars[2 * C::kStages + 6]);
-  const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages + 7]);
+  auto bar_q = [&](int i) { return tc::smem_u32(&bars[2 * C::kStages + 6 + i]); };
+  auto bar_qfree = [&](int i) { return tc::smem_u32(&bars[2 * C::kStages + 8 + i]); };
+  const uint32_t bar_done = tc::smem_u32(&bars[2 * C::kStages + 10]);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  // tiles the block's rows see, and this split's share of them
-  const int first_pos = rp.len - rp.n + r_base / g;
-  const int last_row = min(r_base + 2 * kTile, rows) - 1;
-  const int last_pos = rp.len - rp.n + last_row / g;
-  const int t_hi = p.causal ? min(last_pos + 1, rp.len) : rp.len;
-  const int t_lo = p.window > 0 ? max(0, first_pos - p.window + 1) : 0;
-  int ta = 0, tb = 0;
-  if (t_hi > t_lo) {
-    const int a0 = (t_lo - rp.lo) / kTile, nt = (t_hi - rp.lo + kTile - 1) / kTile - a0;
-    ta = a0 + (int)((int64_t)nt * split / p.splits);
-    tb = a0 + (int)((int64_t)nt * (split + 1) / p.splits);
-  }
-  const int nt = tb - ta;
 
   if (tid == 0) {
     *s_abort = 0u;
     for (int s = 0; s < 2 * C::kStages + 2; ++s) tc::mbar_init(tc::smem_u32(&bars[s]), 1);
     for (int i = 0; i < 4; ++i) tc::mbar_init(bar_p(i >> 1, i & 1), 4);
-    tc::mbar_init(bar_q, 4 * nact);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar_q(i), 1);
+      tc::mbar_init(bar_qfree(i), 4);
+    }
     tc::mbar_init(bar_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -424,48 +661,77 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   auto tm_s = [&](int i) { return tmem + (uint32_t)(i * kTile); };          // S, and P over it
   auto tm_o = [&](int i) { return tmem + (uint32_t)(2 * kTile + i * D); };
 
+  // Each role walks the segments by itself; the barriers' phases run on from
+  // one segment to the next.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 9 && lane == 0 && nt > 0) {
-    // ------------------------------------------------------------- copies
+    // the ring's next stage and its parity
+    int st = 0;
+    uint32_t par = 0;
+    auto next_stage = [&]() {
+      if (++st == C::kStages) {
+        st = 0;
+        par ^= 1u;
+      }
+    };
+    Walk w = walk;
+    if (warp == 9 && lane == 0) {
+      // ----------------------------------------------------------- copies
       const char* kt = reinterpret_cast<const char*>(p.kt);
       const char* vt = reinterpret_cast<const char*>(p.vt);
       bool ok = true;
-      int issued = 0;
-      for (int k = 0; k < 2 * nt; ++k) {
-        const int st = k % C::kStages;
-        if (!tc::mbar_wait(bar_empty(st), ((uint32_t)(k / C::kStages) & 1u) ^ 1u, s_abort)) {
-          ok = false;
-          break;
+      uint32_t used = 0u, last = 0u;               // stages written, their latest parity
+      uint32_t pqf[2] = {1u, 1u}, qs = 0u;         // parity of bar_qfree, q tiles loaded
+      while (ok && w.u < w.end) {
+        int at;
+        const int n = w.take(), nt = w.tiles(n, &at);
+        const int64_t tile0 = w.rp.tile0 + at;
+        for (int k = 0; k < 2 * nt && ok; ++k) {
+          if (k == 1) {                            // the first keys do not wait for the rows' turn
+            const int nact = w.rp.n * g - w.mb * kRows > kTile ? 2 : 1;
+            const char* qt = reinterpret_cast<const char*>(p.qt) +
+                             ((int64_t)(w.rp.pair0 + w.mb) * p.Hkv + w.h) * 2 * C::kTileB;
+            for (int i = 0; i < nact && ok; ++i) {
+              ok = tc::mbar_wait(bar_qfree(i), pqf[i], s_abort);
+              if (!ok) break;
+              pqf[i] ^= 1u;
+              tc::mbar_expect_tx(bar_q(i), (uint32_t)C::kTileB);
+              bulk_load(s0 + C::kOffQ + i * C::kTileB, qt + i * C::kTileB, (uint32_t)C::kTileB,
+                        bar_q(i));
+              qs |= 1u << i;
+            }
+          }
+          if (!ok || !tc::mbar_wait(bar_empty(st), par ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          const int64_t tile = (tile0 + (k >> 1)) * p.Hkv + w.h;
+          tc::mbar_expect_tx(bar_full(st), (uint32_t)C::kTileB);
+          bulk_load(s0 + st * C::kTileB, ((k & 1) ? vt : kt) + tile * C::kTileB,
+                    (uint32_t)C::kTileB, bar_full(st));
+          used |= 1u << st;
+          last = (last & ~(1u << st)) | (par << st);
+          next_stage();
         }
-        const int64_t tile = (int64_t)(rp.tile0 + ta + (k >> 1)) * p.Hkv + h;
-        tc::mbar_expect_tx(bar_full(st), (uint32_t)C::kTileB);
-        bulk_load(s0 + st * C::kTileB, ((k & 1) ? vt : kt) + tile * C::kTileB, (uint32_t)C::kTileB,
-                  bar_full(st));
-        issued = k + 1;
+        w.next(p, n);
       }
       if (!ok) {
         if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x78000000u | (blockIdx.x & 0xFFFFFFu));
         *s_abort = 1u;
       }
       // every copy issued has landed before the CTA may leave
-      for (int k = max(0, issued - C::kStages); k < issued; ++k) {
-        uint32_t never = 0u;
-        tc::mbar_wait(bar_full(k % C::kStages), (uint32_t)(k / C::kStages) & 1u, &never, 100000000ull);
-      }
-    }
-    if (warp == 8 && nt > 0) {
-    // --------------------------------------------------------------- MMAs
-      bool ok = warp_wait(bar_q, 0u, s_abort);
-      // the ring's next stage and its parity
-      int st = 0;
-      uint32_t par = 0;
-      auto next = [&]() {
-        if (++st == C::kStages) {
-          st = 0;
-          par ^= 1u;
+      for (int s = 0; s < C::kStages; ++s)
+        if ((used >> s) & 1u) {
+          uint32_t never = 0u;
+          tc::mbar_wait(bar_full(s), (last >> s) & 1u, &never, 100000000ull);
         }
-      };
+      for (int i = 0; i < 2; ++i)
+        if ((qs >> i) & 1u) {                      // bar_q's parity follows bar_qfree's
+          uint32_t never = 0u;
+          tc::mbar_wait(bar_q(i), pqf[i], &never, 100000000ull);
+        }
+    } else if (warp == 8) {
+      // ------------------------------------------------------------- MMAs
       const uint32_t q_desc = desc_k(s0 + C::kOffQ);
       auto mma_s = [&](int i, uint32_t kd) {
         const uint32_t qd = q_desc + i * (C::kTileB >> 4);
@@ -475,46 +741,62 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
                   kb > 0);
         commit_elected(bar_s(i));
       };
-      ok = ok && warp_wait(bar_full(0), 0u, s_abort);
-      if (ok) {
-        tc::tc_fence_after();
-        const uint32_t kd = desc_k(s0);
-        mma_s(0, kd);
-        if (nact > 1) mma_s(1, kd);
-        commit_elected(bar_empty(0));
-      }
-      next();
-      for (int j = 0; ok && j < nt; ++j) {
-        const bool more = j + 1 < nt;
-        const int sv = st;
-        ok = warp_wait(bar_full(sv), par, s_abort);
-        next();
-        const int sk = st;
-        if (more) {
-          ok = ok && warp_wait(bar_full(sk), par, s_abort);
-          next();
+      bool ok = true;
+      uint32_t pq[2] = {0u, 0u}, pp[2] = {0u, 0u};   // parities of bar_q and bar_p
+      while (ok && w.u < w.end) {
+        int at;
+        const int n = w.take(), nt = w.tiles(n, &at);
+        const int nact = w.rp.n * g - w.mb * kRows > kTile ? 2 : 1;   // MMA tiles with rows
+        if (nt > 0) {
+          const int sk0 = st;
+          ok = warp_wait(bar_full(sk0), par, s_abort);
+          next_stage();
+          const uint32_t kd0 = desc_k(s0 + sk0 * C::kTileB);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (i < nact && ok) {
+              ok = warp_wait(bar_q(i), pq[i], s_abort);
+              pq[i] ^= 1u;
+              if (!ok) break;
+              tc::tc_fence_after();
+              mma_s(i, kd0);
+            }
+          if (ok) commit_elected(bar_empty(sk0));
         }
-        const uint32_t vd = desc_mn(s0 + sv * C::kTileB), kd = desc_k(s0 + sk * C::kTileB);
+        for (int j = 0; ok && j < nt; ++j) {
+          const bool more = j + 1 < nt;
+          const int sv = st;
+          ok = warp_wait(bar_full(sv), par, s_abort);
+          next_stage();
+          const int sk = st;
+          if (more) {
+            ok = ok && warp_wait(bar_full(sk), par, s_abort);
+            next_stage();
+          }
+          const uint32_t vd = desc_mn(s0 + sv * C::kTileB), kd = desc_k(s0 + sk * C::kTileB);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i >= nact || !ok) break;
+          for (int i = 0; i < 2; ++i) {
+            if (i >= nact || !ok) break;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && warp_wait(bar_p(i, half), (uint32_t)j & 1u, s_abort);
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && warp_wait(bar_p(i, half), pp[i], s_abort);
+              if (!ok) break;
+              tc::tc_fence_after();
+              mma_ts4(tm_o(i), tm_s(i) + half * 32, vd + half * (64 * 128 >> 4), C::kIdescO,
+                      half > 0 ? 1u : (uint32_t)j);
+            }
             if (!ok) break;
-            tc::tc_fence_after();
-            mma_ts4(tm_o(i), tm_s(i) + half * 32, vd + half * (64 * 128 >> 4), C::kIdescO,
-                    half > 0 ? 1u : (uint32_t)j);
+            pp[i] ^= 1u;
+            if (more)
+              mma_s(i, kd);
+            else
+              commit_elected(bar_s(i));   // O complete
           }
           if (!ok) break;
-          if (more)
-            mma_s(i, kd);
-          else
-            commit_elected(bar_s(i));   // O complete
+          commit_elected(bar_empty(sv));
+          if (more) commit_elected(bar_empty(sk));
         }
-        if (!ok) break;
-        commit_elected(bar_empty(sv));
-        if (more) commit_elected(bar_empty(sk));
+        w.next(p, n);
       }
       if (!ok) {
         if (lane == 0 && !*s_abort)
@@ -529,183 +811,203 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-    if ((warp >> 2) < nact) {
-    // ------------------------------------------------------------ softmax
+    // --------------------------------------------------------------- softmax
     const int i = warp >> 2;
     const int rr = (warp & 3) * 32 + lane;         // row of the MMA tile, TMEM lane
-    const int r = r_base + i * kTile + rr;         // packed row
-    const bool live = r < rows;
-    const int tok = live ? r / g : 0, hq = h * g + (live ? r - tok * g : 0);
-    const int64_t row = (int64_t)(rp.row0 + tok) * p.Hq + hq;
-    float c;                                       // S c = log2 of the softmax term
-    {
-      uint4 v[D / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) v[k] = live ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t mx = 0u;                            // largest |q| as bf16 bits
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) mx = max(mx, max(x[u] & 0x7FFFu, (x[u] >> 16) & 0x7FFFu));
-      }
-      float up, up2;
-      row_scale(mx, 14, &up, &up2);
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const __half2 hh = __floats2half2_rn(bf16_lo(x[u]) * up * up2, bf16_hi(x[u]) * up * up2);
-          y[u] = *reinterpret_cast<const uint32_t*>(&hh);
-        }
-        *reinterpret_cast<uint4*>(smem + C::kOffQ + i * C::kTileB + tile_off(rr, k)) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-      }
-      c = p.scale * 1.44269504f / up / up2;
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar_q);
-    }
-    const int pos = rp.len - rp.n + (live ? tok : last_row / g);
-    const int see1 = p.causal ? min(pos, rp.len - 1) : rp.len - 1;     // last token seen
-    const int see0 = p.window > 0 ? pos - p.window + 1 : 0;            // first one
-    // tiles that lie within every row's sight need no mask
-    const int w_hi = __reduce_min_sync(0xffffffffu, see1), w_lo = __reduce_max_sync(0xffffffffu, see0);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    float m = -INFINITY, l = 0.0f;
+    // out leaves by whole rows: D / 8 lanes of 16 bytes each
+    constexpr int kLanesRow = D / 8, kRowsStep = 32 / kLanesRow, kSteps = 32 / kRowsStep;
+    const int chunk = lane % kLanesRow, sub = lane / kLanesRow, wrow = (warp & 3) * 32;
+    uint8_t* q_tile = smem + C::kOffQ + i * C::kTileB;   // out is staged there
+    uint32_t ps = 0u;                              // parity of bar_s
     bool ok = true;
+    Walk w = walk;
+    if (tid == 0 && !p.whole) {
+      Cut cut;
+      cut.u0 = u0;
+      cut.lo = u0 - w.off;
+      cut.hi = cut.lo + w.units();
+      cut.row0 = w.rp.row0;
+      cut.rows = w.rp.n * g;
+      cut.mb = w.mb;
+      cut.h = w.h;
+      reinterpret_cast<Cut*>(p.cuts)[blockIdx.x] = cut;
+    }
 #pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), (uint32_t)j & 1u, s_abort));
-      if (!ok) break;
-      tc::tc_fence_after();
-      const int t0 = rp.lo + (ta + j) * kTile;
-      uint32_t v[4][32];
+    for (bool first = true; w.u < w.end; first = false) {
+      int at;
+      const int n = w.take(), nt = w.tiles(n, &at);
+      const ReqPlan& rp = w.rp;
+      const int rows = rp.n * g, r = w.mb * kRows + i * kTile + rr;   // packed row
+      const int t_first = rp.lo + at * kTile;
+      // partial sums: of the share's first segment or of its last
+      const int slot = n < w.units() ? 2 * (int)blockIdx.x + (first ? 0 : 1) : -1;
+      if (w.mb * kRows + i * kTile < rows && ok) {
+        const bool live = r < rows;
+        const int tok = live ? r / g : 0, hq = w.h * g + (live ? r - tok * g : 0);
+        const int row = live ? (rp.row0 + tok) * p.Hq + hq : -1;
+        // S c = log2 of the softmax term; rows past the last see nothing
+        const float c = live ? __ldg(p.qscale + ((int64_t)(rp.pair0 + w.mb) * p.Hkv + w.h) * kRows +
+                                     i * kTile + rr)
+                             : 1.0f;
+        const int pos = rp.len - rp.n + (live ? tok : (rows - 1) / g);
+        const int see1 = p.causal ? min(pos, rp.len - 1) : rp.len - 1;     // last token seen
+        const int see0 = p.window > 0 ? pos - p.window + 1 : 0;            // first one
+        // tiles that lie within every row's sight need no mask
+        const int w_hi = __reduce_min_sync(0xffffffffu, see1),
+                  w_lo = __reduce_max_sync(0xffffffffu, see0);
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < nt; ++j) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), ps, s_abort));
+          ps ^= 1u;
+          if (!ok) break;
+          tc::tc_fence_after();
+          const int t0 = t_first + j * kTile;
+          uint32_t v[4][32];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tc::tmem_ld32(tm_s(i) + lanes + k * 32, v[k]);
-      tc::tmem_ld_wait();
-      if (t0 + kTile - 1 > w_hi || t0 < w_lo) {
-        const int lim1 = see1 - t0, lim0 = see0 - t0;
+          for (int k = 0; k < 4; ++k) tc::tmem_ld32(tm_s(i) + lanes + k * 32, v[k]);
+          tc::tmem_ld_wait();
+          if (t0 + kTile - 1 > w_hi || t0 < w_lo) {
+            const int lim1 = see1 - t0, lim0 = see0 - t0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if (k * 32 + u > lim1 || k * 32 + u < lim0) v[k][u] = 0xFF800000u;   // -inf
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              for (int u = 0; u < 32; ++u)
+                if (k * 32 + u > lim1 || k * 32 + u < lim0) v[k][u] = 0xFF800000u;   // -inf
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int u = 0; u < 32; u += 2)
+          for (int u = 0; u < 32; u += 2)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mx[k] = max3(mx[k], __uint_as_float(v[k][u]), __uint_as_float(v[k][u + 1]));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      if (__any_sync(0xffffffffu, mt > m + kSlack)) {
-        // lane by lane, so that a row's result does not hang on its neighbours'
-        const float mn = mt > m + kSlack ? mt : m;
-        const float f = m == mn ? 1.0f : ex2(m - mn);
-        if (j > 0) {
-          l *= f;
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], __uint_as_float(v[k][u]), __uint_as_float(v[k][u + 1]));
+          const float mt = live ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c : -INFINITY;
+          if (__any_sync(0xffffffffu, mt > m + kSlack)) {
+            // lane by lane, so that a row's result does not hang on its neighbours'
+            const float mn = mt > m + kSlack ? mt : m;
+            const float f = m == mn ? 1.0f : ex2(m - mn);
+            if (j > 0) {
+              l *= f;
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t o[32];
+                tc::tmem_ld32(tm_o(i) + lanes + k * 32, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                tmem_st32(tm_o(i) + lanes + k * 32, o);
+              }
+            }
+            m = mn;
+          }
+          const float base = m == -INFINITY ? 0.0f : kPUp - m;
+          const uint64_t c2 = pack2(c, c), base2 = pack2(base, base);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h2[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              const uint64_t x = fma2(
+                  pack2(__uint_as_float(v[k][2 * u]), __uint_as_float(v[k][2 * u + 1])), c2, base2);
+              float y0, y1;
+              if (u % kPolyOf == kPolyOf - 1) {
+                ex2_fma(x, &y0, &y1);
+              } else {
+                unpack2(x, &y0, &y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+              }
+              sum[u & 1] = add2(sum[u & 1], pack2(y0, y1));
+              const __half2 hh = __floats2half2_rn(y0, y1);
+              h2[u] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            tmem_st16(tm_s(i) + lanes + k * 16, h2);
+            if (k & 1) {   // 64 tokens of P are there: their product may begin
+              tmem_st_wait();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(bar_p(i, k >> 1));
+            }
+          }
+          float l0, l1;
+          unpack2(add2(sum[0], sum[1]), &l0, &l1);
+          l += l0 + l1;
+        }
+        if (nt > 0 && ok) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), ps, s_abort));
+          ps ^= 1u;
+          tc::tc_fence_after();
+        }
+        if (!ok && lane == 0) {
+          if (!*s_abort)
+            record_error(p.hdr, SDK_ERR_TIMEOUT, 0x7A000000u | (blockIdx.x & 0xFFFFFFu));
+          *s_abort = 1u;
+        }
+        // m carries P's offset from here on: O and l are sums of 2^(x - m)
+        const float mo = m == -INFINITY ? -INFINITY : m - kPUp;
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        if (live && ok) {
+          if (slot >= 0)
+            p.part_ml[(int64_t)slot * kRows + i * kTile + rr] = make_float2(mo, l);
+          else if (p.lse != nullptr)
+            p.lse[row] = l > 0.0f || l != l ? (mo + log2f(l)) * 0.69314718f : -INFINITY;
+        }
+        // whole rows go out through the free q tile; partial sums lie
+        // [dim][row], as they come
+        float* part = p.part_o + ((int64_t)slot * 2 + i) * D * kTile + rr;
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[32];
+          if (nt > 0 && ok) {
             tc::tmem_ld32(tm_o(i) + lanes + k * 32, o);
             tc::tmem_ld_wait();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-            tmem_st32(tm_o(i) + lanes + k * 32, o);
-          }
-        }
-        m = mn;
-      }
-      const float base = m == -INFINITY ? 0.0f : kPUp - m;
-      const uint64_t c2 = pack2(c, c), base2 = pack2(base, base);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t h2[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const uint64_t x =
-              fma2(pack2(__uint_as_float(v[k][2 * u]), __uint_as_float(v[k][2 * u + 1])), c2, base2);
-          float y0, y1;
-          if (u % kPolyOf == kPolyOf - 1) {
-            ex2_fma(x, &y0, &y1);
           } else {
-            unpack2(x, &y0, &y1);
-            y0 = ex2(y0);
-            y1 = ex2(y1);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = 0u;
           }
-          sum[u & 1] = add2(sum[u & 1], pack2(y0, y1));
-          const __half2 hh = __floats2half2_rn(y0, y1);
-          h2[u] = *reinterpret_cast<const uint32_t*>(&hh);
+          if (slot < 0 && nt > 0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 bb =
+                    __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                          __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+                y[e] = *reinterpret_cast<const uint32_t*>(&bb);
+              }
+              *reinterpret_cast<uint4*>(q_tile + tile_off(rr, 4 * k + u)) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (slot >= 0 && nt > 0 && live && ok) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) part[(k * 32 + u) * kTile] = __uint_as_float(o[u]);
+          }
         }
-        tmem_st16(tm_s(i) + lanes + k * 16, h2);
-        if (k & 1) {   // 64 tokens of P are there: their product may begin
-          tmem_st_wait();
+        if (slot < 0 && ok) {
+          __syncwarp();
+#pragma unroll 4
+          for (int k = 0; k < kSteps; ++k) {
+            const int rk = __shfl_sync(0xffffffffu, row, k * kRowsStep + sub);
+            if (rk >= 0)
+              *(reinterpret_cast<uint4*>(p.out + (int64_t)rk * D) + chunk) =
+                  nt > 0 ? *reinterpret_cast<const uint4*>(
+                               q_tile + tile_off(wrow + k * kRowsStep + sub, chunk))
+                         : make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (nt > 0) {                              // O is read, the q tile is free
+          tc::fence_proxy_async();
           tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar_p(i, k >> 1));
+          if (lane == 0) tc::mbar_arrive(bar_qfree(i));
         }
       }
-      float l0, l1;
-      unpack2(add2(sum[0], sum[1]), &l0, &l1);
-      l += l0 + l1;
-    }
-    if (nt > 0 && ok) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(bar_s(i), (uint32_t)nt & 1u, s_abort));
-      tc::tc_fence_after();
-    }
-    if (!ok && lane == 0) {
-      if (!*s_abort) record_error(p.hdr, SDK_ERR_TIMEOUT, 0x7A000000u | (blockIdx.x & 0xFFFFFFu));
-      *s_abort = 1u;
-    }
-    // m carries P's offset from here on: O and l are sums of 2^(x - m)
-    const float mo = m == -INFINITY ? -INFINITY : m - kPUp;
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    if (p.splits == 1 && p.lse != nullptr && live && ok)
-      p.lse[row] = l > 0.0f || l != l ? (mo + log2f(l)) * 0.69314718f : -INFINITY;
-    if (p.splits > 1 && live && ok) {
-      p.part_ml[(int64_t)split * p.n_tok * p.Hq + row] = make_float2(mo, l);
-    }
-#pragma unroll 1
-    for (int k = 0; k < D / 32; ++k) {
-      uint32_t o[32];
-      if (nt > 0 && ok) {
-        tc::tmem_ld32(tm_o(i) + lanes + k * 32, o);
-        tc::tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int u = 0; u < 32; ++u) o[u] = 0u;
-      }
-      if (live && ok) {
-        if (p.splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + k * 32);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 bb =
-                  __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * e]) * inv,
-                                        __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
-              y[e] = *reinterpret_cast<const uint32_t*>(&bb);
-            }
-            dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(
-              p.part_o + ((int64_t)split * p.n_tok * p.Hq + row) * D + k * 32);
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        }
-      }
+      w.next(p, n);
     }
     tc::tc_fence_before();
-    }
   }
   __syncthreads();
   if (warp == 8) {
@@ -715,63 +1017,77 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   }
 }
 
-// Joins the splits' partial sums, one warp per (row, query head).
+constexpr int kJoinRows = 32;      // rows of a block of chunk_join_kernel
+
+// Joins the partial sums of the blocks of rows that several shares cut, in
+// the shares' order.  Grid (share, part of the rows): share c stands for the
+// block that its first unit lies inside of, if that is the first cut there.
+// A lane takes a row, a warp D / 8 dims.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
-  constexpr int E = D / 32;
   pdl_wait();
-  const int64_t R = p.n_tok * p.Hq;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  // rows of no request, or of a refused one, stay as they were
-  const int tok = (int)(row / p.Hq);
-  const ReqPlan rp = p.plan[find_request(p, tok)];
-  if (row >= R || tok < rp.row0 || tok >= rp.row0 + rp.n) return;
-  float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[s * R + row].x);
-  float z = 0.0f, o[E];
+  const Cut* cuts = reinterpret_cast<const Cut*>(p.cuts);
+  const int c = (int)blockIdx.x + 1, shares = p.plan[p.B].npair;
+  const Cut cut = cuts[c];                         // (of a share that is not there: not used)
+  const int64_t before = cuts[c - 1].u0;
+  if (c >= shares || cut.u0 == cut.lo || before > cut.lo) return;   // no cut, or an earlier one
+  constexpr int E = D / 8;                         // dims a thread
+  const int rb = blockIdx.y * kJoinRows + (threadIdx.x & 31), dim = threadIdx.x / 32 * E;
+  const int r = cut.mb * kRows + rb;
+  if (r >= cut.rows) return;
+  const int tok = r / p.g;
+  const int64_t row = (int64_t)(cut.row0 + tok) * p.Hq + cut.h * p.g + (r - tok * p.g);
+  // share c - 1 ends with its part, the shares c .. last start with theirs
+  const int slot0 = 2 * (c - 1) + (before < cut.lo ? 1 : 0);
+  auto slot = [&](int s) { return (int64_t)(s < c ? slot0 : 2 * s); };
+  int last = c;
+  while (last + 1 < shares && cuts[last + 1].u0 < cut.hi) ++last;
+  // the first two parts are loaded together with what they weigh
+  auto ml_of = [&](int s) { return p.part_ml[slot(s) * kRows + rb]; };
+  auto sums_of = [&](int s) {
+    return p.part_o + ((slot(s) * 2 + rb / kTile) * D + dim) * kTile + rb % kTile;
+  };
+  float o[E], x[E];
+  const float* s0 = sums_of(c - 1);
+  const float* s1 = sums_of(c);
 #pragma unroll
-  for (int k = 0; k < E; ++k) o[k] = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * R + row];
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // saw nothing
-    const float f = ex2(ml.x - m);
-    z = fmaf(ml.y, f, z);
-    const float* src = p.part_o + (s * R + row) * D + lane * E;
-#pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = fmaf(src[k], f, o[k]);
+  for (int k = 0; k < E; ++k) {
+    o[k] = s0[k * kTile];
+    x[k] = s1[k * kTile];
   }
-  const bool any = z > 0.0f || z != z;
+  const float2 ml0 = ml_of(c - 1), ml1 = ml_of(c);
+  float m = fmaxf(ml0.x, ml1.x);
+  for (int s = c + 1; s <= last; ++s) m = fmaxf(m, ml_of(s).x);
+  // what saw nothing left no sums: whatever is read there does not count
+  auto none = [](float2 ml) { return ml.x == -INFINITY && ml.y == 0.0f; };
+  const float f0 = none(ml0) ? 0.0f : ex2(ml0.x - m), f1 = none(ml1) ? 0.0f : ex2(ml1.x - m);
+  float z = fmaf(ml1.y, f1, ml0.y * f0);
 #pragma unroll
   for (int k = 0; k < E; ++k)
-    p.out[row * D + lane * E + k] = __bfloat16_as_ushort(__float2bfloat16_rn(any ? o[k] / z : 0.0f));
-  if (p.lse != nullptr && lane == 0)
-    p.lse[row] = any ? (m + log2f(z)) * 0.69314718f : -INFINITY;
-}
-
-// How the call is cut: row blocks per request and KV head, and splits of
-// the contexts.  A context is split while the blocks do not fill the SMs,
-// down to four tiles a split (below that the copies' latency and the join
-// outweigh what more CTAs bring).
-struct ChunkCut {
-  int mblocks, splits;
-};
-static ChunkCut chunk_cut(int B, int64_t n_tok, int Hq, int Hkv, int max_q, int max_len,
-                          int window) {
-  const int g = Hq / Hkv;
-  const int64_t q = max_q < n_tok ? max_q : n_tok;
-  ChunkCut c;
-  c.mblocks = (int)((q * g + 2 * kTile - 1) / (2 * kTile));
-  int64_t blocks = n_tok * g / (2 * kTile) + B;
-  if (blocks > (int64_t)B * c.mblocks) blocks = (int64_t)B * c.mblocks;
-  blocks *= Hkv;
-  int64_t span = max_len;
-  if (window > 0 && window + q < span) span = window + q;
-  const int64_t tiles = (span + kTile - 1) / kTile;
-  int64_t s = blocks > 0 ? num_sms() / blocks : 1;
-  if (s > tiles / 4) s = tiles / 4;
-  c.splits = (int)(s < 1 ? 1 : s);
-  return c;
+    o[k] = fmaf(none(ml1) ? 0.0f : x[k], f1, none(ml0) ? 0.0f : o[k] * f0);
+  for (int s = c + 1; s <= last; ++s) {
+    const float2 ml = ml_of(s);
+    const float* src = sums_of(s);
+#pragma unroll
+    for (int k = 0; k < E; ++k) x[k] = src[k * kTile];
+    const float f = none(ml) ? 0.0f : ex2(ml.x - m);
+    z = fmaf(ml.y, f, z);
+#pragma unroll
+    for (int k = 0; k < E; ++k) o[k] = fmaf(none(ml) ? 0.0f : x[k], f, o[k]);
+  }
+  const float inv = z > 0.0f || z != z ? 1.0f / z : 0.0f;
+#pragma unroll
+  for (int k = 0; k < E; k += 8) {
+    uint32_t y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
+      y[e] = *reinterpret_cast<const uint32_t*>(&a);
+    }
+    *reinterpret_cast<uint4*>(p.out + row * D + dim + k) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  if (p.lse != nullptr && dim == 0)
+    p.lse[row] = z > 0.0f || z != z ? (m + log2f(z)) * 0.69314718f : -INFINITY;
 }
 
 int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
@@ -793,12 +1109,31 @@ static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int ma
   return pairs <= 8 && tokens >= 65536;
 }
 
+// CTAs of the attention kernel: one per SM, or as many as there can be tiles.
+// Where all blocks fit the SMs and their contexts are short, each has a CTA of
+// its own and nothing is cut or joined (eight chats of up to 600 tokens: 20
+// us, with shares 32 us).
+struct ChunkCut {
+  int ctas;
+  bool whole;
+};
+static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
+  const int64_t tiles = (max_len + (int64_t)kTile - 1) / kTile, items = blocks * Hkv;
+  ChunkCut c;
+  c.whole = items <= num_sms() && tiles <= 8;
+  const int64_t most = c.whole ? items : items * (tiles + kBlockCost);
+  c.ctas = (int)(most < num_sms() ? (most < 1 ? 1 : most) : num_sms());
+  return c;
+}
+
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len) {
-  // without a window: a window only lowers the number of splits
-  const ChunkCut c = chunk_cut(B, n_tok, Hq, Hkv, max_q, max_len, 0);
-  const size_t a =
-      chunk_layout(B, n_tok * Hq, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.splits).total;
+  const int64_t q = max_q < n_tok ? max_q : n_tok;
+  const int64_t blocks = cap_blocks(B, n_tok, Hq / Hkv, (int)q);
+  const ChunkCut c = chunk_cut(blocks, Hkv, max_len);
+  const size_t a = chunk_layout(B, blocks, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.ctas,
+                                c.whole)
+                       .total;
   if (!by_atoms(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len)) return a;
   const size_t b = atoms_workspace_bytes(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
   return a > b ? a : b;
@@ -806,7 +1141,7 @@ size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n
 
 template <int D>
 static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
-  const size_t smem = (size_t)(p.B + 1) * 4;
+  const size_t smem = (size_t)2 * (p.B + 1) * 4;   // 33 KB at most: no opt-in
   static unsigned long long attr_set = 0ull;
   if (device_needs_setup(&attr_set)) {
     if (cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -814,26 +1149,32 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
       return SDK_ERR_CUDA;
     device_setup_done(&attr_set);
   }
-  // a warp takes one step of tokens where that many warps are not more than
-  // the device holds at once, else four
+  // a warp takes one step of tokens while that gives at most a few rounds of
+  // the device's warps, else four
   constexpr int kStep = 32 / (2 * (D / 8)) * (kRebThreads / 32);   // tokens of a CTA's step
   const int64_t steps = (int64_t)p.cap_tiles * p.Hkv * (kTile / kStep);
-  int64_t grid;
-  if (steps <= 8 * num_sms()) {
-    grid = steps;
+  constexpr int kPackRows = 32 / (D / 8) * kPackSteps * (kRebThreads / 32);   // rows of a CTA's step
+  int64_t prep = (p.n_tok * p.Hq + kPackRows - 1) / kPackRows;
+  if (prep > 8 * num_sms()) prep = 8 * num_sms();
+  if (steps <= 24 * num_sms()) {
+    const int64_t grid = 1 + (steps < 2 * num_sms() - 1 ? steps : 2 * num_sms() - 1);
     rebuild_kernel<D, 1><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
   } else {
-    grid = steps / 4 < 8 * num_sms() ? steps / 4 : 8 * num_sms();
-    rebuild_kernel<D, 4><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
+    chunk_prep_kernel<D><<<(unsigned)prep, kRebThreads, smem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess ||
+        launch_after(rebuild_kernel<D, 4>, dim3((unsigned)(8 * num_sms())), kRebThreads, smem, stream,
+                     p) != cudaSuccess)
+      return SDK_ERR_CUDA;
   }
-  if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
-  const int64_t ctas = (int64_t)p.B * p.Hkv * p.mblocks * p.splits;
-  if (ctas > 0x7FFFFFFF) return SDK_ERR_INVALID_ARG;
-  if (launch_after(chunk_attn_kernel<D>, dim3((unsigned)ctas), kAThreads, ACfg<D>::kSmem, stream,
+  if (launch_after(chunk_attn_kernel<D>, dim3((unsigned)p.ctas), kAThreads, ACfg<D>::kSmem, stream,
                    p) != cudaSuccess)
     return SDK_ERR_CUDA;
-  if (p.splits > 1 && launch_after(chunk_join_kernel<D>, dim3((unsigned)((p.n_tok * p.Hq + 7) / 8)),
-                                   256, 0, stream, p) != cudaSuccess)
+  const int64_t most_rows = (int64_t)p.max_q * p.g < kRows ? (int64_t)p.max_q * p.g : kRows;
+  if (p.ctas > 1 && !p.whole &&
+      launch_after(chunk_join_kernel<D>,
+                   dim3((unsigned)(p.ctas - 1), (unsigned)((most_rows + kJoinRows - 1) / kJoinRows)),
+                   256, 0, stream, p) != cudaSuccess)
     return SDK_ERR_CUDA;
   return SDK_OK;
 }
@@ -847,10 +1188,16 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
     const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
     if (taken) return s;
   }
-  const ChunkCut c = chunk_cut(p.B, p.n_tok, p.Hq, p.Hkv, p.max_q, p.max_len, p.window);
-  const ChunkLayout l = chunk_layout(p.B, p.n_tok * p.Hq, p.Hkv, p.d, p.cap_tiles, c.splits);
-  p.mblocks = c.mblocks;
-  p.splits = c.splits;
+  const int64_t blocks = cap_blocks(p.B, p.n_tok, p.g, p.max_q);
+  p.cap_work = blocks;
+  const ChunkCut c = chunk_cut(blocks, p.Hkv, p.max_len);
+  p.ctas = c.ctas;
+  p.whole = c.whole ? 1 : 0;
+  const ChunkLayout l = chunk_layout(p.B, blocks, p.Hkv, p.d, p.cap_tiles, c.ctas, c.whole);
+  p.cuts = workspace + l.cuts;
+  p.units = reinterpret_cast<int64_t*>(workspace + l.units);
+  p.qscale = reinterpret_cast<float*>(workspace + l.qs);
+  p.qt = reinterpret_cast<__half*>(workspace + l.qt);
   p.kt = reinterpret_cast<__half*>(workspace + l.kt);
   p.vt = reinterpret_cast<__half*>(workspace + l.vt);
   p.part_ml = reinterpret_cast<float2*>(workspace + l.ml);

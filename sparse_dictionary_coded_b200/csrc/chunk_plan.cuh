@@ -7,6 +7,7 @@
 namespace sdk {
 
 constexpr int kTile = 128;   // tokens of a rebuilt tile; a request's first token rounds down to one
+constexpr int kRows = 256;   // packed rows of a block: two MMA tiles
 
 // Inclusive scan of one 64-bit value per thread (blockDim.x a multiple of
 // 32, <= 1024).
@@ -59,16 +60,19 @@ __device__ __forceinline__ ReqPlan check_request(const ChunkParams& p, int b, un
 }
 
 // Scans all requests.  s_first [B + 1]: first tile (ATOMS: first row pair)
-// of every request; CTA 0 leaves the plan and its totals in the workspace.
-// A request whose tiles (ATOMS: row pairs or work) pass what the host's
-// bounds gave room for is refused.
+// of every request, s_block [B + 1] (not ATOMS): its first block of packed
+// rows; the leader CTA leaves the plan and its totals in the workspace.  A
+// request whose tiles or blocks (ATOMS: row pairs or work) pass what the host's
+// bounds gave room for is refused (offsets that fall count rows twice).
 template <bool ATOMS>
-__device__ void make_plan(const ChunkParams& p, bool leader, int32_t* s_first, int64_t* s_warp) {
+__device__ void make_plan(const ChunkParams& p, bool leader, int32_t* s_first, int32_t* s_block,
+                          int64_t* s_warp) {
   const int64_t cap = ATOMS ? p.cap_pairs : p.cap_tiles;
   int64_t first = 0, work = 0;
   __shared__ unsigned long long s_used, s_work;   // what the accepted requests take
   if (threadIdx.x == 0) {
     s_first[0] = 0;
+    if (!ATOMS) s_block[0] = 0;
     s_used = s_work = 0ull;
   }
   __syncthreads();
@@ -80,23 +84,30 @@ __device__ void make_plan(const ChunkParams& p, bool leader, int32_t* s_first, i
     const int64_t units = ATOMS ? (int64_t)r.npair * p.Hkv : r.ntiles;
     int64_t tot_u, tot_w = 0;
     const int64_t upto = first + block_scan64(units, s_warp, &tot_u);
-    const int64_t mine = ATOMS ? units * (r.len - r.lo) : 0;
-    const int64_t done = ATOMS ? work + block_scan64(r.n > 0 ? mine : 0, s_warp, &tot_w) : 0;
+    // units of work (ATOMS), or blocks of rows
+    const int64_t mine = ATOMS ? units * (r.len - r.lo) : ((int64_t)r.n * p.g + kRows - 1) / kRows;
+    const int64_t done = work + block_scan64(mine, s_warp, &tot_w);
     if (b < p.B) {
       // once over, the sums stay over: every later request with units is
       // refused too, and the totals end with the last accepted one
-      if (units > 0 && (upto > cap || (ATOMS && done > p.cap_work))) {
+      if ((units > 0 || mine > 0) && (upto > cap || done > p.cap_work)) {
         err = SDK_ERR_CAPACITY;
         r.n = 0;
       } else if (leader && units > 0) {
         atomicMax(&s_used, (unsigned long long)upto);
         atomicMax(&s_work, (unsigned long long)done);
       }
+      if (!ATOMS) s_block[b + 1] = (int)min(done, p.cap_work);
       s_first[b + 1] = (int)min(upto, cap);
       if (leader) {
         r.tile0 = (int)min(upto - units, cap);
-        r.pair0 = r.tile0;
-        r.work0 = min(done - mine, (int64_t)p.cap_work);
+        if (ATOMS) {
+          r.pair0 = r.tile0;
+          r.work0 = min(done - mine, p.cap_work);
+        } else {
+          r.pair0 = (int)min(done - mine, p.cap_work);
+          r.npair = (int)mine;
+        }
         if (r.n == 0) r.ntiles = r.npair = 0;
         p.plan[b] = r;
         if (err) record_error(p.hdr, err, 0x75000000u | (uint32_t)b);

@@ -38,9 +38,9 @@ struct ReqPlan {
   int lo;         // first token any row sees, rounded down to a tile
   int tile0;      // its first tile in the workspace
   int ntiles;
-  int pair0;      // its first pair of packed rows
-  int npair;      // pairs per KV head
-  int64_t work0;  // (pair, token) units before it
+  int pair0;      // its first block of 256 packed rows (by atoms: first row pair)
+  int npair;      // blocks per request and KV head (by atoms: pairs)
+  int64_t work0;  // units of work before it: tiles of blocks (by atoms: tokens of pairs)
 };
 
 struct ChunkParams {
@@ -55,8 +55,12 @@ struct ChunkParams {
   float* lse;
   WsHeader* hdr;
   ReqPlan* plan;         // [B + 1], the last one the totals
-  // by tiles: rebuilt key and value tiles [tile][Hkv][tile image], partial
-  // sums of the splits [split][row][..]
+  // by tiles: running sums of the blocks' tiles, rebuilt key and value tiles
+  // [tile][Hkv][tile image], partial sums [2 x CTA][256 rows][..]
+  int64_t* units;
+  char* cuts;            // what every share starts with
+  __half* qt;            // scaled query tiles [block][Hkv][2][tile image]
+  float* qscale;         // [block][Hkv][256 rows] score to log2 of its exponential
   __half* kt;
   __half* vt;
   float2* part_ml;
@@ -69,8 +73,8 @@ struct ChunkParams {
   char* wimg;
   int64_t n_tok, cap_pairs, cap_work;
   int B, Hq, Hkv, g, d, n, n_pad, n_pages, page_size, max_pages;
-  int max_q, max_len, window, causal, cap_tiles, mblocks, splits;
-  int ctas, ksplits, row_tiles;
+  int max_q, max_len, window, causal, cap_tiles;
+  int ctas, whole, ksplits, row_tiles;
   float scale;
 };
 
