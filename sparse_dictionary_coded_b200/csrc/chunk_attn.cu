@@ -38,7 +38,7 @@ ChunkLayout chunk_layout(int B, int64_t blocks, int Hkv, int d, int64_t cap_tile
   const size_t tiles = (size_t)cap_tiles * Hkv * kTile * d * 2;
   l.units = up256(sizeof(WsHeader) + ((size_t)B + 1) * sizeof(ReqPlan));
   l.cuts = up256(l.units + ((size_t)blocks + 1) * 8);
-  l.qs = up256(l.cuts + (size_t)ctas * sizeof(Cut));
+  l.qs = up256(l.cuts + (whole ? 0 : (size_t)ctas * sizeof(Cut)));
   l.qt = up256(l.qs + (size_t)blocks * Hkv * kRows * 4);
   l.kt = l.qt + (size_t)blocks * Hkv * kRows * d * 2;
   l.vt = l.kt + tiles;
@@ -560,7 +560,6 @@ struct Walk {
   }
   // block m of the call alone, for KV head hh; false: there is none
   __device__ __forceinline__ bool whole(const ChunkParams& p, int m, int hh) {
-    if (m >= p.plan[p.B].pair0) return false;
     b = warp_search(p.B, m, [&](int i) { return (int64_t)p.plan[i].pair0; });
     rp = p.plan[b];
     h = hh;
@@ -610,8 +609,12 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   int64_t u0 = 0, u1 = 0;
   Walk walk;
   if (p.whole) {                                   // CTA = block
-    const int m = (int)blockIdx.x / p.Hkv;
-    if (!walk.whole(p, m, (int)blockIdx.x - m * p.Hkv)) return;
+    // a head's blocks side by side, so that their CTAs read the same tiles at
+    // the same time; the longest of a causal call first
+    const int blocks = p.plan[p.B].pair0;
+    if (blocks == 0) return;
+    const int head = (int)blockIdx.x / blocks, m = blocks - 1 - (int)blockIdx.x % blocks;
+    if (head >= p.Hkv || !walk.whole(p, m, head)) return;
   } else {
     const int64_t total = p.plan[p.B].work0;
     const int shares = p.plan[p.B].npair;
@@ -1109,20 +1112,25 @@ static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int ma
   return pairs <= 8 && tokens >= 65536;
 }
 
-// CTAs of the attention kernel: one per SM, or as many as there can be tiles.
-// Where all blocks fit the SMs and their contexts are short, each has a CTA of
-// its own and nothing is cut or joined (eight chats of up to 600 tokens: 20
-// us, with shares 32 us).
+// CTAs of the attention kernel: one per block, or one per SM with equal
+// shares.  A CTA per block where all contexts are short and the blocks fit the
+// SMs (eight chats of up to 600 tokens: 20 us, with shares 32 us), and where
+// the blocks fill whole rounds of the SMs (their CTAs read a tile together;
+// 2048 tokens over 32768, 256 blocks: 1250 us, with shares 1300 us).  Shares
+// where there are too few blocks (twelve mixed requests: 33 us, with a CTA per
+// block 37 us).
 struct ChunkCut {
   int ctas;
   bool whole;
 };
 static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
-  const int64_t tiles = (max_len + (int64_t)kTile - 1) / kTile, items = blocks * Hkv;
+  const int64_t tiles = (max_len + (int64_t)kTile - 1) / kTile, items = blocks * Hkv, sms = num_sms();
+  const int64_t rounds = (items + sms - 1) / sms;
   ChunkCut c;
-  c.whole = items <= num_sms() && tiles <= 8;
-  const int64_t most = c.whole ? items : items * (tiles + kBlockCost);
-  c.ctas = (int)(most < num_sms() ? (most < 1 ? 1 : most) : num_sms());
+  c.whole = rounds <= 1 ? tiles <= 8 : 5 * items >= 4 * rounds * sms;
+  if (items > 0x7FFFFFFF) c.whole = false;
+  const int64_t most = c.whole ? items : min(items * (tiles + kBlockCost), sms);
+  c.ctas = (int)(most < 1 ? 1 : most);
   return c;
 }
 
@@ -1156,7 +1164,7 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
   constexpr int kPackRows = 32 / (D / 8) * kPackSteps * (kRebThreads / 32);   // rows of a CTA's step
   int64_t prep = (p.n_tok * p.Hq + kPackRows - 1) / kPackRows;
   if (prep > 8 * num_sms()) prep = 8 * num_sms();
-  if (steps <= 24 * num_sms()) {
+  if (steps <= 80 * num_sms()) {
     const int64_t grid = 1 + (steps < 2 * num_sms() - 1 ? steps : 2 * num_sms() - 1);
     rebuild_kernel<D, 1><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
