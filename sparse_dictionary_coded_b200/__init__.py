@@ -306,8 +306,25 @@ def sdk_decode_attn(q, dict_k, dict_v, store, klow=3, khigh=16, top_num=1,
 # ------------------------------------------------------------- paged store
 #
 # These calls belong to a serving step, where a single token's plan takes
-# the device a few microseconds: the checks below are written for the host's
-# time (one pass over the tensors, raw addresses handed to ctypes).
+# the device a few microseconds: checks, outputs and launch are done in
+# _binding.so (csrc/binding.cpp); sdk_paged_append, whose encoder takes longer,
+# is marshalled here.  A call with `stream` makes its outputs and workspace on
+# that stream too.
+
+_calls = None
+
+
+def _load_binding():
+    global _calls
+    load()
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        raise RuntimeError("_binding.so is not built (run `python -m "
+                           "sparse_dictionary_coded_b200.build`): %s" % e) from e
+    _calls = b
+    return b
+
 
 def _shape(t, name, *dims):
     if tuple(t.shape) != dims:
@@ -317,43 +334,10 @@ def _shape(t, name, *dims):
 
 def _on(dev, name, t, dtype):
     """The address of t, a contiguous tensor of dtype on the device dev."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev \
-            or not t.is_contiguous():
-        _cuda_contig(t, name, (dtype,))
+    _cuda_contig(t, name, (dtype,))
+    if t.device != dev:
         raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, dev))
     return t.data_ptr()
-
-
-def _device_of(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    return t.device
-
-
-def _launch(fn, where, dev, stream, args):
-    """fn(*args, stream) with dev as the current device, on `stream` or dev's
-    current stream."""
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch._C._cuda_getDevice() == dev.index:
-        rc = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, raw)
-    if rc != SDK_OK:
-        raise SdkError(rc, where)
-
-
-def _workspace(nbytes, dev, stream):
-    """A workspace for one call, its header cleared on the call's stream."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
-    _launch(load().sdk_workspace_init, "sdk_workspace_init", dev, stream,
-            (ws.data_ptr(), ws.numel()))
-    return ws
 
 
 def _page_shape(pages):
@@ -384,38 +368,16 @@ def sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size,
     free_pages, which may hold fewer entries than the pool has pages).
     Returns BlockTables; requests that do not fit are refused and recorded
     in the workspace (include/sdk.h)."""
-    dev = _device_of(lens, "lens")
-    i32 = torch.int32
-    a_lens, a_new = _on(dev, "lens", lens, i32), _on(dev, "n_new", n_new, i32)
-    a_free, a_nf = _on(dev, "free_pages", free_pages, i32), _on(dev, "n_free", n_free, i32)
-    a_table = _on(dev, "block_table", block_table, i32)
-    if lens.dim() != 1 or free_pages.dim() != 1 or block_table.dim() != 2:
-        raise ValueError("lens and free_pages have one dimension, block_table two")
-    B = lens.shape[0]
-    rows, cols = block_table.shape
-    if n_new.shape != lens.shape or rows != B or n_free.numel() != 1:
-        raise ValueError("lens and n_new are [B], block_table is [B, max_pages], n_free [1]")
-    n_stack = free_pages.shape[0]
-    if slot_map is None:
-        slot_map = torch.empty(max_new, dtype=torch.int64, device=dev)
-    if cu_new is None:
-        cu_new = torch.empty(B + 1, dtype=i32, device=dev)
-    if new_lens is None:
-        new_lens = torch.empty(B, dtype=i32, device=dev)
-    if n_free_out is None:
-        n_free_out = torch.empty(1, dtype=i32, device=dev)
-    if slot_map.numel() != max_new or cu_new.numel() != B + 1 or new_lens.numel() != B \
-            or n_free_out.numel() != 1:
-        raise ValueError("slot_map is [max_new], cu_new [B + 1], new_lens [B], n_free_out [1]")
-    if workspace is None:
-        workspace = _workspace(sdk_block_tables_workspace_bytes(B), dev, stream)
-    _launch(load().sdk_block_tables, "sdk_block_tables", dev, stream, (
-        a_lens, a_new, B, a_free, n_stack, a_nf, n_stack if n_pages is None else n_pages, page_size,
-        a_table, cols, max_new, _on(dev, "slot_map", slot_map, torch.int64),
-        _on(dev, "cu_new", cu_new, i32), _on(dev, "new_lens", new_lens, i32),
-        _on(dev, "n_free_out", n_free_out, i32), _on(dev, "workspace", workspace, torch.uint8),
-        workspace.numel()))
-    return BlockTables(block_table, slot_map, cu_new, new_lens, n_free_out)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size, max_new,
+                                    n_pages, slot_map, cu_new, new_lens, n_free_out, workspace)
+    r = (_calls or _load_binding()).block_tables(
+        lens, n_new, free_pages, n_free, block_table, page_size, max_new, n_pages, slot_map, cu_new,
+        new_lens, n_free_out, workspace)
+    if r.__class__ is int:
+        raise SdkError(r, "sdk_block_tables")
+    return BlockTables._make(r)
 
 
 def sdk_paged_store_workspace_bytes():
@@ -428,24 +390,13 @@ def sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace=None,
     [n_tok * Hkv, 16], as sdk_encode returns them) to their slots of pages
     int32 [n_pages, Hkv, page_size, 2, 16]; slot_map int64 [n_tok], negative
     slots are skipped.  Returns pages."""
-    dev = _device_of(pages, "pages")
-    a_pages = _on(dev, "pages", pages, torch.int32)
-    n_pages, Hkv, page_size = _page_shape(pages)
-    a_slots = _on(dev, "slot_map", slot_map, torch.int64)
-    a_k = _on(dev, "codes_k", codes_k, torch.int32)
-    a_v = _on(dev, "codes_v", codes_v, torch.int32)
-    n_tok = slot_map.numel()
-    words = n_tok * Hkv * K_ATOMS
-    if codes_k.numel() != words or codes_v.numel() != words or codes_k.shape[-1] != K_ATOMS \
-            or codes_v.shape[-1] != K_ATOMS:
-        raise ValueError("codes_k and codes_v must hold %d words of %d heads for %d tokens" %
-                         (K_ATOMS, Hkv, n_tok))
-    if workspace is None:
-        workspace = _workspace(sdk_paged_store_workspace_bytes(), dev, stream)
-    _launch(load().sdk_paged_store, "sdk_paged_store", dev, stream, (
-        a_k, a_v, n_tok, Hkv, a_slots, a_pages, n_pages, page_size,
-        _on(dev, "workspace", workspace, torch.uint8), workspace.numel()))
-    return pages
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace)
+    r = (_calls or _load_binding()).paged_store(pages, codes_k, codes_v, slot_map, workspace)
+    if r.__class__ is int:
+        raise SdkError(r, "sdk_paged_store")
+    return r
 
 
 def sdk_paged_append_workspace_bytes(n_tok, Hkv, head_dim, n_atoms):
@@ -457,8 +408,10 @@ def sdk_paged_append(pages, xk, xv, dict_k, dict_v, slot_map, workspace=None,
     """Encodes xk, xv [n_tok, Hkv, head_dim] (fp32 or bf16) and writes their
     codes to the slots slot_map int64 [n_tok] of pages.  Returns the
     workspace (its header records what the device found)."""
-    dev = _device_of(pages, "pages")
-    a_pages = _on(dev, "pages", pages, torch.int32)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sdk_paged_append(pages, xk, xv, dict_k, dict_v, slot_map, workspace)
+    dev = _cuda_contig(pages, "pages", (torch.int32,)).device
     n_pages, Hkv, page_size = _page_shape(pages)
     xk = _cuda_contig(xk, "xk", (torch.float32, torch.bfloat16))
     a_xk, a_xv = _on(dev, "xk", xk, xk.dtype), _on(dev, "xv", xv, xk.dtype)
@@ -470,12 +423,14 @@ def sdk_paged_append(pages, xk, xv, dict_k, dict_v, slot_map, workspace=None,
     _shape(dict_v, "dict_v", n_atoms, d)
     _shape(xk, "xk", n_tok, Hkv, d)
     _shape(xv, "xv", n_tok, Hkv, d)
-    if workspace is None:
-        workspace = _workspace(sdk_paged_append_workspace_bytes(n_tok, Hkv, d, n_atoms), dev,
-                               stream)
-    _launch(load().sdk_paged_append, "sdk_paged_append", dev, stream, (
-        a_xk, a_xv, _x_dtype(xk), n_tok, Hkv, d, a_dk, a_dv, n_atoms, a_slots, a_pages, n_pages,
-        page_size, _on(dev, "workspace", workspace, torch.uint8), workspace.numel()))
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = new_workspace(sdk_paged_append_workspace_bytes(n_tok, Hkv, d, n_atoms), dev)
+        rc = load().sdk_paged_append(
+            a_xk, a_xv, _x_dtype(xk), n_tok, Hkv, d, a_dk, a_dv, n_atoms, a_slots,
+            pages.data_ptr(), n_pages, page_size, _on(dev, "workspace", workspace, torch.uint8),
+            workspace.numel(), _stream())
+    _check(rc, "sdk_paged_append")
     return workspace
 
 
@@ -496,44 +451,16 @@ def sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q,
     and on all contexts together (0: B * max_len).  Returns out bf16 [n_tok,
     Hq, head_dim]; lse: a float32 [n_tok, Hq] tensor that receives the
     logarithms of the softmax sums."""
-    dev = _device_of(q, "q")
-    bf16, i32 = torch.bfloat16, torch.int32
-    a_q = _on(dev, "q", q, bf16)
-    a_pages = _on(dev, "pages", pages, i32)
-    n_pages, Hkv, page_size = _page_shape(pages)
-    a_dk, a_dv = _on(dev, "dict_k", dict_k, bf16), _on(dev, "dict_v", dict_v, bf16)
-    a_table, a_lens = _on(dev, "block_table", block_table, i32), _on(dev, "lens", lens, i32)
-    a_cu = _on(dev, "cu_q", cu_q, i32)
-    if q.dim() != 3 or lens.dim() != 1 or block_table.dim() != 2 or dict_k.dim() != 2:
-        raise ValueError("q has three dimensions, lens one, block_table and dict_k two")
-    n_tok, Hq, d = q.shape
-    n_atoms = dict_k.shape[0]
-    B = lens.shape[0]
-    rows, cols = block_table.shape
-    if dict_k.shape[1] != d or dict_v.shape != dict_k.shape:
-        raise ValueError("dict_k and dict_v are [n_atoms, %d]" % d)
-    if rows != B or cu_q.numel() != B + 1:
-        raise ValueError("lens is [B], block_table [B, max_pages], cu_q [B + 1]")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty((n_tok, Hq, d), dtype=bf16, device=dev)
-    elif out.shape != q.shape:
-        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), tuple(q.shape)))
-    a_lse = None
-    if lse is not None:
-        _shape(lse, "lse", n_tok, Hq)
-        a_lse = _on(dev, "lse", lse, torch.float32)
-    if workspace is None:
-        workspace = _workspace(
-            sdk_chunk_attn_workspace_bytes(B, n_tok, Hq, Hkv, d, n_atoms, max_q, max_len,
-                                           total_len), dev, stream)
-    _launch(load().sdk_chunk_attn, "sdk_chunk_attn", dev, stream, (
-        a_q, n_tok, B, Hq, Hkv, d, a_dk, a_dv, n_atoms, a_pages, n_pages, page_size, a_table, cols,
-        a_lens, a_cu, max_q, max_len, total_len, window, SDK_CHUNK_CAUSAL if causal else 0, scale,
-        _on(dev, "out", out, bf16), a_lse, _on(dev, "workspace", workspace, torch.uint8),
-        workspace.numel()))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q, max_len,
+                                  total_len, causal, window, scale, out, lse, workspace)
+    r = (_calls or _load_binding()).chunk_attn(
+        q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q, max_len, total_len, causal, window,
+        scale, out, lse, workspace)
+    if r.__class__ is int:
+        raise SdkError(r, "sdk_chunk_attn")
+    return r
 
 
 class PagedCodeStore:

@@ -1,4 +1,6 @@
-"""Build libsdk.so in place: nvcc for sm_100a, no GPU needed to compile.
+"""Build libsdk.so (nvcc for sm_100a) and the Python binding of the calls where
+the host's time counts (_binding.so, g++ over torch's headers) in place; no GPU
+needed to compile.
 
     python -m sparse_dictionary_coded_b200.build
 """
@@ -14,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdk.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["api.cu", "chunk_atoms.cu", "chunk_attn.cu", "decode.cu", "decode_static.cu", "encode_simt.cu", "encode_small.cu",
            "encode_tc.cu", "out_tc.cu", "paged.cu", "qd_tc.cu"]
@@ -66,7 +69,29 @@ def build(verbose=False, force=False):
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError("link failed")
+    build_binding(force)
     return LIB
+
+
+def build_binding(force=False):
+    """Compile and link _binding.so against torch and libsdk.so."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not (force or _stale(BINDING, src)):
+        return
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           src, "-o", BINDING, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", LIB, "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed: " + " ".join(cmd))
 
 
 if __name__ == "__main__":
