@@ -7,12 +7,12 @@ namespace sdk {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr uint32_t kCap = 0x7FFFFFFFu;   // sums saturate here (a + b fits 32 bits)
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kCap); }
 
-// Inclusive saturating scan of one value (<= kCap) per thread.
+// Inclusive saturating scan of one value (<= kCap) per thread of a block of T.
+template <int T>
 __device__ __forceinline__ uint32_t block_sat_scan(uint32_t v, uint32_t* s_warp, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -23,17 +23,17 @@ __device__ __forceinline__ uint32_t block_sat_scan(uint32_t v, uint32_t* s_warp,
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    uint32_t t = s_warp[lane];
+    uint32_t t = lane < T / 32 ? s_warp[lane] : 0u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t u = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t = sat_add(t, u);
     }
-    s_warp[lane] = t;
+    if (lane < T / 32) s_warp[lane] = t;
   }
   __syncthreads();
   const uint32_t r = warp > 0 ? sat_add(v, s_warp[warp - 1]) : v;
-  *total = s_warp[kPlanThreads / 32 - 1];
+  *total = s_warp[T / 32 - 1];
   __syncthreads();
   return r;
 }
@@ -43,12 +43,14 @@ __device__ __forceinline__ uint32_t block_sat_scan(uint32_t v, uint32_t* s_warp,
 // One step's plan.  Every CTA scans the requests itself (rows, then pages:
 // two scans of at most 4096 values in shared memory cost a few hundred ns, a
 // second launch or a grid-wide wait would cost more), then takes its share
-// of the table entries and of the slots by binary search in the scans.  The
-// page of a slot comes from the free stack when this call assigns it, so no
-// CTA reads an entry another one writes.  Bound by its launch and the
-// chain load - scan - load for a step of single tokens, by the 8-byte
-// writes of slot_map for prompts.
-__global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableParams p) {
+// of the table entries and of the slots by binary search in the scans, four
+// rows a thread at a time.  The page of a slot comes from the free stack when
+// this call assigns it, so no CTA reads an entry another one writes.  Bound
+// by its launch and the chain load - scan - load for a step of single tokens
+// (3.7 us for 4 requests), by the 8-byte writes of slot_map for prompts.
+// T threads: 256 for up to 256 requests, else 1024.
+template <int T>
+__global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
   extern __shared__ int32_t sm[];
   int32_t* s_row = sm;                  // [B + 1] first row of every request
   int32_t* s_fresh = s_row + p.B + 1;   // [B + 1] pages taken before it
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableParams 
   }
   if (tid == 0) s_row[0] = s_fresh[0] = 0;
   uint32_t row0 = 0, page0 = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += T) {
     const int b = b0 + tid;
     int len = 0, n = 0;
     if (b < p.B) {
@@ -71,7 +73,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableParams 
       n = p.n_new[b];
     }
     uint32_t rows, pages;
-    const uint32_t row1 = sat_add(row0, block_sat_scan((uint32_t)max(n, 0), s_warp, &rows));
+    const uint32_t row1 = sat_add(row0, block_sat_scan<T>((uint32_t)max(n, 0), s_warp, &rows));
     // refused: 1 a bound or the pool, 2 a bad length
     int refused = 0;
     uint32_t need = 0, have = 0;
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableParams 
       else
         need = want - have;
     }
-    const uint32_t upto = sat_add(page0, block_sat_scan(need, s_warp, &pages));
+    const uint32_t upto = sat_add(page0, block_sat_scan<T>(need, s_warp, &pages));
     if (!refused && upto > (uint32_t)n_free && need > 0) refused = 1;
     if (b < p.B) {
       s_row[b + 1] = (int)min(row1, (uint32_t)p.max_new);
@@ -111,21 +113,21 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableParams 
   __syncthreads();
   {
     int m = 0;
-    for (int b = tid; b < p.B; b += kPlanThreads) m = max(m, s_fresh[b + 1]);
+    for (int b = tid; b < p.B; b += T) m = max(m, s_fresh[b + 1]);
     m = (int)__reduce_max_sync(0xffffffffu, m);
     if ((tid & 31) == 0 && m > 0) atomicMax(&s_taken, m);
   }
   __syncthreads();
   const int taken = s_taken;
-  for (int b = tid; b < p.B; b += kPlanThreads)
+  for (int b = tid; b < p.B; b += T)
     if (s_fresh[b + 1] < 0) s_fresh[b + 1] = taken;
   __syncthreads();
   if (blockIdx.x == 0) {
-    for (int b = tid; b <= p.B; b += kPlanThreads) p.cu_new[b] = s_row[b];
+    for (int b = tid; b <= p.B; b += T) p.cu_new[b] = s_row[b];
     if (tid == 0) *p.n_free_out = n_free - taken;
   }
-  const int64_t step = (int64_t)gridDim.x * kPlanThreads;
-  const int64_t t0 = (int64_t)blockIdx.x * kPlanThreads + tid;
+  const int64_t step = (int64_t)gridDim.x * T;
+  const int64_t t0 = (int64_t)blockIdx.x * T + tid;
   auto fresh_page = [&](int e) {       // the e-th page taken
     const int pg = p.free_pages[n_free - 1 - e];
     if (pg >= 0 && pg < p.n_pages) return pg;
@@ -147,78 +149,99 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableParams 
     p.table[(int64_t)b * p.max_pages + have + ((int)e - s_fresh[b])] = fresh_page((int)e);
   }
   const int n_rows = s_row[p.B];
-  for (int64_t r = t0; r < p.max_new; r += step) {
-    int64_t slot = -1;
-    if (r < n_rows) {
+  constexpr int R = 4;                  // rows a thread has in flight
+  for (int64_t r0 = t0; r0 < p.max_new; r0 += R * step) {
+    int64_t slot[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t r = r0 + k * step;
+      slot[k] = -1;
+      if (r >= n_rows) continue;
       const int b = find(s_row, (int)r);
       const int len = s_len[b];
-      if (len >= 0) {
-        const uint32_t pos = (uint32_t)len + (uint32_t)((int)r - s_row[b]);
-        const uint32_t col = pos / P, have = ((uint32_t)len + P - 1) / P;
-        int pg;
-        if (col >= have) {
-          pg = fresh_page(s_fresh[b] + (int)(col - have));
-        } else {
-          pg = p.table[(int64_t)b * p.max_pages + col];
-          if (pg < 0 || pg >= p.n_pages) {
-            record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x73000000u | (uint32_t)b);
-            pg = -1;
-          }
-        }
-        if (pg >= 0) slot = (int64_t)pg * P + (pos - col * P);
-      }
+      if (len < 0) continue;
+      const uint32_t pos = (uint32_t)len + (uint32_t)((int)r - s_row[b]);
+      const uint32_t col = pos / P, have = ((uint32_t)len + P - 1) / P;
+      const bool fresh = col >= have;
+      const int pg = *(fresh ? p.free_pages + (n_free - 1 - (s_fresh[b] + (int)(col - have)))
+                             : p.table + ((int64_t)b * p.max_pages + col));
+      if (pg >= 0 && pg < p.n_pages)
+        slot[k] = (int64_t)pg * P + (pos - col * P);
+      else if (!fresh)                  // (a bad page of the stack is recorded above)
+        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x73000000u | (uint32_t)b);
     }
-    p.slot_map[r] = slot;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (r0 + k * step < p.max_new) p.slot_map[r0 + k * step] = slot[k];
   }
 }
 
 // Eight lanes copy one (token, KV head): four 16-byte pieces of key words,
-// four of value words, to the 128-byte line of its slot.  Bound by HBM (the
-// words are read once and written once).
+// four of value words, to the 128-byte line of its slot; a thread has four
+// pieces in flight.  Bound by HBM (the words are read once and written once).
+// I: the type that counts the pieces.
+template <typename I>
 __global__ void __launch_bounds__(256) paged_store_kernel(StoreParams p) {
-  const int64_t items = p.n_tok * p.Hkv * 8;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < items; e += step) {
-    const int64_t rec = e >> 3;
-    const int c = (int)e & 7;
-    const int64_t t = rec / p.Hkv;
-    const int h = (int)(rec - t * p.Hkv);
-    const int64_t slot = p.slot_map[t];
-    if (slot < 0) continue;
-    if (slot >= (int64_t)p.n_pages * p.page_size) {
-      record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x74000000u);
-      continue;
+  constexpr int R = 4;
+  const I items = (I)p.n_tok * (I)(p.Hkv * 8), step = (I)gridDim.x * 256;
+  for (I e0 = (I)blockIdx.x * 256 + threadIdx.x; e0 < items; e0 += R * step) {
+    uint4 v[R];
+    int64_t at[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const I e = e0 + k * step;
+      at[k] = -1;
+      if (e >= items) continue;
+      const I rec = e >> 3, t = rec / (I)p.Hkv;
+      const int c = (int)(e & 7), h = (int)(rec - t * (I)p.Hkv);
+      v[k] = __ldg(reinterpret_cast<const uint4*>(c < 4 ? p.codes_k : p.codes_v) + rec * 4 + (c & 3));
+      const int64_t slot = __ldg(p.slot_map + t);
+      if (slot < 0) continue;
+      if (slot >= (int64_t)p.n_pages * p.page_size) {
+        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x74000000u);
+        continue;
+      }
+      const uint32_t page = (uint32_t)slot / (uint32_t)p.page_size;
+      const uint32_t off = (uint32_t)slot - page * (uint32_t)p.page_size;
+      at[k] = (((int64_t)page * p.Hkv + h) * p.page_size + off) * 8 + c;
     }
-    const uint32_t page = (uint32_t)slot / (uint32_t)p.page_size;
-    const uint32_t off = (uint32_t)slot - page * (uint32_t)p.page_size;
-    const uint4* src = reinterpret_cast<const uint4*>(c < 4 ? p.codes_k : p.codes_v);
-    uint4* dst = reinterpret_cast<uint4*>(p.pages) +
-                 (((int64_t)page * p.Hkv + h) * p.page_size + off) * 8;
-    dst[c] = src[rec * 4 + (c & 3)];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (at[k] >= 0) reinterpret_cast<uint4*>(p.pages)[at[k]] = v[k];
   }
 }
 
-sdk_status launch_block_tables(const TableParams& p, cudaStream_t stream) {
+template <int T>
+static sdk_status launch_tables(const TableParams& p, cudaStream_t stream) {
   const int64_t work = p.max_new > p.B ? p.max_new : p.B;
-  int64_t grid = (work + kPlanThreads - 1) / kPlanThreads;
-  if (grid > 2 * num_sms()) grid = 2 * num_sms();
-  const size_t smem = (size_t)(3 * p.B + 2) * 4;
+  int64_t grid = (work + 4 * T - 1) / (4 * T);
+  const int64_t most = (int64_t)num_sms() * (2048 / T);
+  if (grid > most) grid = most;
   static unsigned long long attr_set = 0ull;
   if (device_needs_setup(&attr_set)) {
-    if (cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(block_tables_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (3 * SDK_MAX_REQUESTS + 2) * 4) != cudaSuccess)
       return SDK_ERR_CUDA;
     device_setup_done(&attr_set);
   }
-  block_tables_kernel<<<(unsigned)grid, kPlanThreads, smem, stream>>>(p);
+  block_tables_kernel<T><<<(unsigned)grid, T, (size_t)(3 * p.B + 2) * 4, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SDK_OK : SDK_ERR_CUDA;
+}
+
+sdk_status launch_block_tables(const TableParams& p, cudaStream_t stream) {
+  return p.B <= 256 ? launch_tables<256>(p, stream) : launch_tables<1024>(p, stream);
 }
 
 sdk_status launch_paged_store(const StoreParams& p, cudaStream_t stream) {
   if (p.n_tok == 0) return SDK_OK;
-  int64_t grid = (p.n_tok * p.Hkv * 8 + 255) / 256;
+  const int64_t items = p.n_tok * p.Hkv * 8;
+  int64_t grid = (items + 1023) / 1024;
   if (grid > 32 * num_sms()) grid = 32 * num_sms();
-  paged_store_kernel<<<(unsigned)grid, 256, 0, stream>>>(p);
+  // e0 + 3 steps stays below 2^32 for the small type
+  if (items <= (int64_t)1 << 31)
+    paged_store_kernel<uint32_t><<<(unsigned)grid, 256, 0, stream>>>(p);
+  else
+    paged_store_kernel<int64_t><<<(unsigned)grid, 256, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SDK_OK : SDK_ERR_CUDA;
 }
 
