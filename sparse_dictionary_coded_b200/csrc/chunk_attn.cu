@@ -77,11 +77,12 @@ __device__ __forceinline__ void block_tiles(const ChunkParams& p, const ReqPlan&
 // besides (queries in, outputs out, a pipeline filled and drained: 12000
 // cycles against 3000 a tile); a block that sees nothing counts as one, so
 // that its rows are written.
+constexpr int kMaxShares = 160;
 constexpr int kBlockCost = 4;
 __device__ __forceinline__ int block_units(int tiles) { return tiles > 0 ? tiles + kBlockCost : 1; }
 
 // One CTA: the running sum of the blocks' units over all requests, every
-// request's first one, and the number of shares: as many as CTAs, but of two
+// request's first one, and the number of shares: as many as CTAs, but of four
 // units at least.
 __device__ void plan_blocks(const ChunkParams& p, const int32_t* s_block, int64_t* s_warp) {
   int64_t sum = 0, total;
@@ -108,7 +109,7 @@ __device__ void plan_blocks(const ChunkParams& p, const int32_t* s_block, int64_
     p.plan[b].pair0 = s_block[b];
     p.plan[b].work0 = p.units[s_block[b]] * p.Hkv;
     if (b == p.B) {
-      const int64_t shares = (p.units[s_block[b]] * p.Hkv + 1) / 2;
+      const int64_t shares = (p.units[s_block[b]] * p.Hkv + 3) / 4;
       p.plan[b].npair = (int)(shares < p.ctas ? (shares < 1 ? 1 : shares) : p.ctas);
     }
   }
@@ -1028,6 +1029,7 @@ constexpr int kJoinRows = 32;      // rows of a block of chunk_join_kernel
 // A lane takes a row, a warp D / 8 dims.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
+  __shared__ float2 s_ml[kMaxShares * kJoinRows];
   pdl_wait();
   const Cut* cuts = reinterpret_cast<const Cut*>(p.cuts);
   const int c = (int)blockIdx.x + 1, shares = p.plan[p.B].npair;
@@ -1037,47 +1039,57 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
   constexpr int E = D / 8;                         // dims a thread
   const int rb = blockIdx.y * kJoinRows + (threadIdx.x & 31), dim = threadIdx.x / 32 * E;
   const int r = cut.mb * kRows + rb;
-  if (r >= cut.rows) return;
-  const int tok = r / p.g;
-  const int64_t row = (int64_t)(cut.row0 + tok) * p.Hq + cut.h * p.g + (r - tok * p.g);
+  if (cut.mb * kRows + (int)blockIdx.y * kJoinRows >= cut.rows) return;
   // share c - 1 ends with its part, the shares c .. last start with theirs
   const int slot0 = 2 * (c - 1) + (before < cut.lo ? 1 : 0);
   auto slot = [&](int s) { return (int64_t)(s < c ? slot0 : 2 * s); };
   int last = c;
   while (last + 1 < shares && cuts[last + 1].u0 < cut.hi) ++last;
-  // the first two parts are loaded together with what they weigh
-  auto ml_of = [&](int s) { return p.part_ml[slot(s) * kRows + rb]; };
+  const int parts = last - c + 2;                  // of the shares c - 1 .. last
+  // the first two parts' sums are on their way while the weights are read
   auto sums_of = [&](int s) {
-    return p.part_o + ((slot(s) * 2 + rb / kTile) * D + dim) * kTile + rb % kTile;
+    return p.part_o + ((slot(c - 1 + s) * 2 + rb / kTile) * D + dim) * kTile + rb % kTile;
   };
-  float o[E], x[E];
-  const float* s0 = sums_of(c - 1);
-  const float* s1 = sums_of(c);
+  float x0[E], x1[E];
 #pragma unroll
   for (int k = 0; k < E; ++k) {
-    o[k] = s0[k * kTile];
-    x[k] = s1[k * kTile];
+    x0[k] = sums_of(0)[k * kTile];
+    x1[k] = sums_of(1)[k * kTile];
   }
-  const float2 ml0 = ml_of(c - 1), ml1 = ml_of(c);
-  float m = fmaxf(ml0.x, ml1.x);
-  for (int s = c + 1; s <= last; ++s) m = fmaxf(m, ml_of(s).x);
+  for (int i = threadIdx.x; i < parts * kJoinRows; i += 256) {
+    const int s = i / kJoinRows;
+    s_ml[i] = p.part_ml[slot(c - 1 + s) * kRows + blockIdx.y * kJoinRows + i % kJoinRows];
+  }
+  __syncthreads();
+  if (r >= cut.rows) return;
+  const float2* ml = s_ml + (threadIdx.x & 31);
+  float m = -INFINITY, z = 0.0f, o[E];
+  for (int s = 0; s < parts; ++s) m = fmaxf(m, ml[s * kJoinRows].x);
   // what saw nothing left no sums: whatever is read there does not count
-  auto none = [](float2 ml) { return ml.x == -INFINITY && ml.y == 0.0f; };
-  const float f0 = none(ml0) ? 0.0f : ex2(ml0.x - m), f1 = none(ml1) ? 0.0f : ex2(ml1.x - m);
-  float z = fmaf(ml1.y, f1, ml0.y * f0);
+  auto weigh = [&](int s, bool* none) {
+    const float2 w = ml[s * kJoinRows];
+    *none = w.x == -INFINITY && w.y == 0.0f;
+    const float f = *none ? 0.0f : ex2(w.x - m);
+    z = fmaf(w.y, f, z);
+    return f;
+  };
+  bool none0, none1;
+  const float f0 = weigh(0, &none0), f1 = weigh(1, &none1);
 #pragma unroll
-  for (int k = 0; k < E; ++k)
-    o[k] = fmaf(none(ml1) ? 0.0f : x[k], f1, none(ml0) ? 0.0f : o[k] * f0);
-  for (int s = c + 1; s <= last; ++s) {
-    const float2 ml = ml_of(s);
+  for (int k = 0; k < E; ++k) o[k] = fmaf(none1 ? 0.0f : x1[k], f1, none0 ? 0.0f : x0[k] * f0);
+#pragma unroll 4
+  for (int s = 2; s < parts; ++s) {
     const float* src = sums_of(s);
+    bool none;
+    const float f = weigh(s, &none);
 #pragma unroll
-    for (int k = 0; k < E; ++k) x[k] = src[k * kTile];
-    const float f = none(ml) ? 0.0f : ex2(ml.x - m);
-    z = fmaf(ml.y, f, z);
-#pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = fmaf(none(ml) ? 0.0f : x[k], f, o[k]);
+    for (int k = 0; k < E; ++k) {
+      const float x = src[k * kTile];
+      o[k] = fmaf(none ? 0.0f : x, f, o[k]);
+    }
   }
+  const int tok = r / p.g;
+  const int64_t row = (int64_t)(cut.row0 + tok) * p.Hq + cut.h * p.g + (r - tok * p.g);
   const float inv = z > 0.0f || z != z ? 1.0f / z : 0.0f;
 #pragma unroll
   for (int k = 0; k < E; k += 8) {
@@ -1100,16 +1112,23 @@ int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
   return sum < each ? sum : each;
 }
 
-// Which form a call takes.  Rebuilding costs 0.74 ns a token and KV head
-// (head_dim 128), however many rows follow; going by atoms costs PER_PAIR
-// for every two rows and FIXED once.
+// Which form a call takes, by what the two were measured to take (us; T:
+// tokens times KV heads).  Rebuilding: 30 and 0.84e-3 T at head_dim 128, half
+// at 64, however many rows follow.  By atoms: 45, the codes' way from HBM
+// (1.7e-4 T), the gathers and additions of every row pair (5.5e-5 T a pair),
+// and 20 for every pair that an SM starts on.  32 query and 8 KV heads, one
+// token: 2048 tokens 41 against 60, 8192 tokens 97 against 69, 32768 tokens 256
+// against 116; four tokens over 32768 254 against 185, eight 250 against 282.
 static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q, int max_len,
                      int64_t total_len) {
-  const int64_t q = max_q < n_tok ? max_q : n_tok;
-  const int64_t pairs = (q * (Hq / Hkv) + 1) / 2;
-  const int64_t tokens = (total_len > 0 ? total_len : (int64_t)B * max_len) * Hkv;
+  const int64_t q = max_q < n_tok ? max_q : n_tok, g = Hq / Hkv;
   if (q < 1) return false;
-  return pairs <= 8 && tokens >= 65536;
+  const double pairs = (double)((q * g + 1) / 2);
+  const double all = min((double)B * pairs, (double)(n_tok * g + B) / 2) * Hkv;
+  double T = (double)B * max_len;
+  if (total_len > 0 && total_len < T) T = (double)total_len;
+  T *= Hkv;
+  return 45 + 1.7e-4 * T + 5.5e-5 * T * pairs + 20 * all / num_sms() < 30 + 0.84e-3 * T * (d / 128.0);
 }
 
 // CTAs of the attention kernel: one per block, or one per SM with equal
@@ -1129,7 +1148,9 @@ static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
   ChunkCut c;
   c.whole = rounds <= 1 ? tiles <= 8 : 5 * items >= 4 * rounds * sms;
   if (items > 0x7FFFFFFF) c.whole = false;
-  const int64_t most = c.whole ? items : min(items * (tiles + kBlockCost), sms);
+  int64_t most = min(sms, (int64_t)kMaxShares);
+  if (c.whole) most = items;
+  else if (items * (tiles + kBlockCost) < 4 * most) most = (items * (tiles + kBlockCost) + 3) / 4;
   c.ctas = (int)(most < 1 ? 1 : most);
   return c;
 }
