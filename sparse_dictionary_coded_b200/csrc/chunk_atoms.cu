@@ -22,7 +22,7 @@ constexpr int kM = 128;            // atoms per QD tile, head dims of w D_V
 constexpr int kChunk = 64;         // atoms per step of w D_V
 constexpr int kTab = SDK_MAX_ATOMS;
 constexpr int kMaxCtas = 512;      // CTAs of the token kernel
-constexpr int kTokThreads = 768;
+constexpr int kTokThreads = 640;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -57,7 +57,7 @@ AtomCut atom_cut(int B, int64_t n_tok, int Hq, int Hkv, int n, int max_q, int ma
 }
 
 struct AtomLayout {
-  size_t qd, scale, score, ml, w, o, total;
+  size_t qd, scale, pair, score, ml, w, o, total;
 };
 
 AtomLayout atom_layout(int B, int d, const AtomCut& c) {
@@ -65,7 +65,8 @@ AtomLayout atom_layout(int B, int d, const AtomCut& c) {
   const size_t rows = (size_t)c.row_tiles * kN;
   l.qd = up256(sizeof(WsHeader) + ((size_t)B + 1) * sizeof(ReqPlan));
   l.scale = up256(l.qd + (size_t)c.pairs * c.n_pad * 4);
-  l.score = up256(l.scale + (size_t)c.pairs * 8);
+  l.pair = up256(l.scale + (size_t)c.pairs * 8);
+  l.score = up256(l.pair + (size_t)c.pairs * 16);
   l.ml = up256(l.score + (size_t)c.work * 8);
   l.w = up256(l.ml + rows * 8);
   l.o = up256(l.w + rows * c.chunks * kChunk * 2 * 2);
@@ -207,8 +208,12 @@ __global__ void __launch_bounds__(192, 1)
     float up, rest;
     row_scale(s_max[tid], 0, &up, &rest);
     s_up[tid] = up;
-    if (blockIdx.x == 0 && pair_base + tid / 2 < n_pairs)
+    const int other = __shfl_down_sync(0xffffffffu, s_row[tid], 1);
+    if (blockIdx.x == 0 && pair_base + tid / 2 < n_pairs) {
       p.row_scale[2 * pair_base + tid] = p.scale * 1.44269504f / up;
+      // the pair's rows; no shares so far
+      if ((tid & 1) == 0) p.pair_of[pair_base + tid / 2] = make_int4(s_row[tid], other, 0, -1);
+    }
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -401,7 +406,7 @@ __device__ __forceinline__ uint32_t clean_word(uint32_t w, bool* bad) {
 // thread's part of sum_t p_t and of sum_t p_t sum_j |c_tj|.  CLEAN: bad words
 // are made harmless and recorded.  Tokens of no weight are not read.
 template <bool FULL, bool CLEAN>
-__device__ __forceinline__ float2 add_weights(const ChunkParams& p, uint32_t* tab,
+__device__ __forceinline__ float2 add_weights_of(const ChunkParams& p, uint32_t* tab,
                                               const float2* score, const int32_t* table, int h,
                                               int ta, int cnt, int e, float m, float up, int len,
                                               int b) {
@@ -465,6 +470,22 @@ __device__ __forceinline__ float2 add_weights(const ChunkParams& p, uint32_t* ta
   return make_float2(z, sum);
 }
 
+template <bool FULL>
+__device__ __forceinline__ float2 add_weights(const ChunkParams& p, uint32_t* tab,
+                                              const float2* score, const int32_t* table, int h,
+                                              int ta, int cnt, int e, float m, float up, int len,
+                                              int b) {
+  return add_weights_of<FULL, false>(p, tab, score, table, h, ta, cnt, e, m, up, len, b);
+}
+// the rare way, kept out of the loop's registers
+template <bool FULL>
+__device__ __forceinline__ float2 add_clean_weights(const ChunkParams& p, uint32_t* tab,
+                                                 const float2* score, const int32_t* table, int h,
+                                                 int ta, int cnt, int e, float m, float up, int len,
+                                                 int b) {
+  return add_weights_of<FULL, true>(p, tab, score, table, h, ta, cnt, e, m, up, len, b);
+}
+
 }  // namespace
 
 // One CTA per SM takes an equal share of the (row pair, token) units, cut
@@ -483,9 +504,12 @@ __device__ __forceinline__ float2 add_weights(const ChunkParams& p, uint32_t* ta
 // Bound by the shared memory: random gathers and additions of 32 lanes need
 // 3.5 passes over the banks on average.
 template <bool FULL>
-__global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams p) {
+__global__ void __launch_bounds__(kTokThreads, 1)
+    atoms_token_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ __align__(16) uint32_t tab[];   // [kTab]
   __shared__ float s_red[32];
+  __shared__ float s_sample[kTokThreads / 32][8];
+  __shared__ float s_bound[2];
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ uint32_t s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -527,6 +551,10 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
     const int slot = (int)blockIdx.x + pair;
     const int ta = rp.lo + u0, tb = ta + cnt;
     float2* score = p.score + w;
+    if (tid == 0) {                           // the shares that hold the pair's tokens
+      if (u0 == 0) p.pair_of[pair].z = (int)blockIdx.x;
+      if (u0 + cnt == span) p.pair_of[pair].w = (int)blockIdx.x;
+    }
     const int32_t* table = p.table + (int64_t)b * p.max_pages;
 
     tc::fence_proxy_async();
@@ -651,6 +679,49 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
     m0 = block_reduce(m0, -INFINITY, s_red, fmax2);
     m1 = block_reduce(m1, -INFINITY, s_red, fmax2);
 
+    // ---- the size of p c from one token per thread; only tokens that a row
+    // sees have a say in its rounding
+    {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // per row: seen, |c|, p, p |c|
+      if (mine < cnt) {
+        const float2 s2 = score[mine];
+        at.init(ta + mine, P);
+        const float p0 = m0 > -INFINITY ? ex2(s2.x - m0) : 0.0f,
+                    p1 = m1 > -INFINITY ? ex2(s2.y - m1) : 0.0f;
+        const bool in0 = p0 > 0.0f, in1 = p1 > 0.0f;             // (false for NaN)
+        const uint32_t rec = record_of(p, page_of(table, at, true), at.off, h, in0 || in1, b);
+        if (rec != kNoRecord) {
+          const uint4* words = reinterpret_cast<const uint4*>(p.pages) + (int64_t)rec * 8 + 4;
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = __ldg(words + k);
+          float a = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            a += (fabsf(word_coef(x[k].x)) + fabsf(word_coef(x[k].y))) +
+                 (fabsf(word_coef(x[k].z)) + fabsf(word_coef(x[k].w)));
+          if (in0) v[0] = 1.0f, v[1] = a, v[2] = p0, v[3] = p0 * a;
+          if (in1) v[4] = 1.0f, v[5] = a, v[6] = p1, v[7] = p1 * a;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s_sample[warp][k] = v[k];
+      __syncthreads();
+      if (tid < 2) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < kTokThreads / 32; ++k)
+          for (int q4 = 0; q4 < 4; ++q4) t[q4] += s_sample[k][4 * tid + q4];
+        const float seen = fmaxf(t[0], 1.0f), share = (float)cnt / (float)min(cnt, kTokThreads);
+        s_bound[tid] = 8.0f * fmaxf(t[1] / seen, fmaxf(t[3], t[2] * (t[1] / seen)) * share);
+      }
+      __syncthreads();
+    }
+
     // ---- weights, row by row
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
@@ -666,26 +737,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
                                : make_float2(-INFINITY, 0.0f);
         continue;
       }
-      // the size of p c from one token per thread; only tokens that the row
-      // sees have a say in its rounding
-      float sa = 0.0f, sp = 0.0f, spa = 0.0f;
-      at.init(min(ta + mine, rp.len), P);
-      if (mine < cnt) {
-        const float2 s2 = score[mine];
-        sp = ex2((e ? s2.y : s2.x) - m);
-        const uint32_t rec = record_of(p, page_of(table, at, true), at.off, h, sp > 0.0f, b);
-        if (rec != kNoRecord) {
-          const uint32_t* words = p.pages + (int64_t)rec * 2 * kAtoms + kAtoms;
-          for (int k = 0; k < kAtoms; ++k) sa += fabsf(word_coef(words[k]));
-          spa = sp * sa;
-        }
-      }
-      const float seen = (float)max(1, __syncthreads_count(sp > 0.0f));
-      sa = block_reduce(sa, 0.0f, s_red, fadd2);
-      sp = block_reduce(sp, 0.0f, s_red, fadd2);
-      spa = block_reduce(spa, 0.0f, s_red, fadd2);
-      float bound = 8.0f * fmaxf(sa / seen, fmaxf(spa, sp * (sa / seen)) / (float)min(cnt, kTokThreads) *
-                                                (float)cnt);
+      float bound = s_bound[e];
       float z = 0.0f, inv = 0.0f;
       bool clean = false;
 #pragma unroll 1
@@ -702,8 +754,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) atoms_token_kernel(ChunkParams
         __syncthreads();
         float za, aa;
         const float2 sums =
-            clean ? add_weights<FULL, true>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b)
-                  : add_weights<FULL, false>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b);
+            clean ? add_clean_weights<FULL>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b)
+                  : add_weights<FULL>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b);
         za = sums.x;
         aa = sums.y;
         z = block_reduce(za, 0.0f, s_red, fadd2);
@@ -892,7 +944,7 @@ __global__ void __launch_bounds__(128, 1)
 
 // The sums of a row's segments over all atom ranges: a block takes 32 dims
 // of a row, a thread per dim and group of partial sums, the groups joined in
-// order.  Latency-bound: the loads of a thread are independent and in
+// order.  Latency-bound: three dependent loads, those of a thread's sums in
 // flight together.
 template <int D>
 __global__ void __launch_bounds__(512) atoms_join_kernel(ChunkParams p) {
@@ -900,48 +952,29 @@ __global__ void __launch_bounds__(512) atoms_join_kernel(ChunkParams p) {
   __shared__ float s_o[512];
   __shared__ float2 s_ml[kMaxCtas];
   pdl_wait();
-  const int64_t row = blockIdx.x / (D / 32);
+  const int pair = (int)blockIdx.x / (2 * (D / 32)), e = (int)blockIdx.x / (D / 32) & 1;
+  const int4 of = p.pair_of[pair];                 // (of a pair that is not there: not used)
+  if (pair >= p.plan[p.B].pair0) return;
+  const int row = e ? of.y : of.x;
+  if (row < 0) return;                             // the pair has one row
   const int dim = (blockIdx.x % (D / 32)) * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
-  const int tok = (int)(row / p.Hq), hq = (int)(row - (int64_t)tok * p.Hq);
-  const ReqPlan rp = p.plan[find_request(p, tok)];
-  // rows of no request, or of a refused one, stay as they were
-  if (tok < rp.row0 || tok >= rp.row0 + rp.n) return;
-  const int h = hq / p.g, r = (tok - rp.row0) * p.g + (hq - h * p.g);
-  const int64_t q = (int64_t)h * rp.npair + (r >> 1), span = rp.len - rp.lo;
-  const int64_t w0 = rp.work0 + q * span, w1 = w0 + span, W = p.plan[p.B].work0;
+  const int c0 = of.z, segs = of.w - of.z + 1;     // 0: nothing to see
+  const int64_t rows = (int64_t)p.row_tiles * kN, first = 2 * (int64_t)(c0 + pair) + e;
   float m = -INFINITY, z = 0.0f, o = 0.0f;
-  if (span > 0) {
-    // the CTAs whose shares meet [w0, w1)
-    int c0 = (int)((double)w0 / (double)W * p.ctas);
-    c0 = min(max(c0, 0), p.ctas - 1);
-    while (c0 > 0 && W * c0 / p.ctas > w0) --c0;
-    while (c0 + 1 < p.ctas && W * (c0 + 1) / p.ctas <= w0) ++c0;
-    int c1 = c0 + 1;
-    while (c1 < p.ctas && W * c1 / p.ctas < w1) ++c1;
-    const int64_t rows = (int64_t)p.row_tiles * kN;
-    const int64_t first = 2 * (int64_t)(rp.pair0 + q) + (r & 1);
-    const int segs = c1 - c0;
-    for (int c = threadIdx.x; c < segs; c += 512)   // an empty share has no sums
-      s_ml[c] = W * (c0 + c) / p.ctas < W * (c0 + c + 1) / p.ctas
-                    ? p.part_ml[first + 2 * (c0 + c)]
-                    : make_float2(-INFINITY, 0.0f);
-    __syncthreads();
-    for (int c = 0; c < segs; ++c) m = fmaxf(m, s_ml[c].x);
-    for (int c = 0; c < segs; ++c)
-      if (s_ml[c].y != 0.0f) z = fmaf(s_ml[c].y, ex2(s_ml[c].x - m), z);
-    __syncthreads();
-    for (int c = threadIdx.x; c < segs; c += 512)
-      s_ml[c].y = s_ml[c].y != 0.0f ? ex2(s_ml[c].x - m) : 0.0f;
-    __syncthreads();
-    const float* src = p.part_o + (first + 2 * (int64_t)c0) * D + dim;
-    const int all = segs * p.ksplits;
+  for (int c = threadIdx.x; c < segs; c += 512) s_ml[c] = p.part_ml[first + 2 * c];
+  __syncthreads();
+  for (int c = 0; c < segs; ++c) m = fmaxf(m, s_ml[c].x);
+  for (int c = 0; c < segs; ++c)
+    if (s_ml[c].y != 0.0f) z = fmaf(s_ml[c].y, ex2(s_ml[c].x - m), z);
+  const float* src = p.part_o + first * D + dim;
+  const int all = segs * p.ksplits;
 #pragma unroll 8
-    for (int i = grp; i < all; i += G) {
-      const int c = i / p.ksplits, k = i - c * p.ksplits;
-      const float f = s_ml[c].y;
-      // what saw nothing has no sums to read
-      o = fmaf(f, f != 0.0f ? src[(k * rows + 2 * c) * D] : 0.0f, o);
-    }
+  for (int i = grp; i < all; i += G) {
+    const int c = i / p.ksplits, k = i - c * p.ksplits;
+    const float2 ml = s_ml[c];
+    const float v = src[(k * rows + 2 * c) * D];
+    // what saw nothing has no sums: whatever is read there does not count
+    o = fmaf(ml.y != 0.0f ? ex2(ml.x - m) : 0.0f, ml.y != 0.0f ? v : 0.0f, o);
   }
   s_o[threadIdx.x] = o;
   __syncthreads();
@@ -949,7 +982,7 @@ __global__ void __launch_bounds__(512) atoms_join_kernel(ChunkParams p) {
 #pragma unroll
   for (int k = 1; k < G; ++k) o += s_o[k * 32 + threadIdx.x];
   const bool any = z > 0.0f || z != z;
-  p.out[row * D + dim] =
+  p.out[(int64_t)row * D + dim] =
       __bfloat16_as_ushort(__float2bfloat16_rn(z != z ? z : any ? o / z : 0.0f));
   if (p.lse != nullptr && dim == 0) p.lse[row] = any ? (m + log2f(z)) * 0.69314718f : -INFINITY;
 }
@@ -987,7 +1020,7 @@ static sdk_status launch_atoms_d(const CUtensorMap& kmap, const CUtensorMap& vma
   if (launch_after(token, dim3((unsigned)p.ctas), kTokThreads, kTab * 4, stream, p) != cudaSuccess ||
       launch_after(atoms_out_kernel<D>, dim3((unsigned)p.ksplits, (unsigned)p.row_tiles), 128,
                    OutCfg::kSmem, stream, vmap, p) != cudaSuccess ||
-      launch_after(atoms_join_kernel<D>, dim3((unsigned)(p.n_tok * p.Hq * (D / 32))), 512, 0,
+      launch_after(atoms_join_kernel<D>, dim3((unsigned)(p.cap_pairs * 2 * (D / 32))), 512, 0,
                    stream, p) != cudaSuccess)
     return SDK_ERR_CUDA;
   return SDK_OK;
@@ -1021,6 +1054,7 @@ sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
   p.n_pad = c.n_pad;
   p.qd = reinterpret_cast<__half2*>(workspace + l.qd);
   p.row_scale = reinterpret_cast<float*>(workspace + l.scale);
+  p.pair_of = reinterpret_cast<int4*>(workspace + l.pair);
   p.score = reinterpret_cast<float2*>(workspace + l.score);
   p.part_ml = reinterpret_cast<float2*>(workspace + l.ml);
   p.wimg = workspace + l.w;

@@ -69,6 +69,7 @@ struct ChunkParams {
   // of (pair, token), and the weights per atom as operand images
   __half2* qd;
   float* row_scale;
+  int4* pair_of;         // a pair's rows, and the first and last share of its tokens
   float2* score;
   char* wimg;
   int64_t n_tok, cap_pairs, cap_work;
