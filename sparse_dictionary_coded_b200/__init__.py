@@ -493,8 +493,11 @@ class PagedCodeStore:
 
     def release(self, page_ids):
         """Puts the pages of a finished request (int32 tensor of distinct
-        pages in use, none negative) back on the stack."""
+        pages in use, none negative) back on the stack.  Pages beyond the
+        pool's number are dropped (a page was released twice)."""
         n = page_ids.numel()
         at = self.n_free.long() + torch.arange(n, device=self.free_pages.device)
-        self.free_pages[at] = page_ids.to(torch.int32)
-        self.n_free = self.n_free + n
+        room = torch.cat([self.free_pages, self.free_pages.new_empty(n)])
+        room[at] = page_ids.to(torch.int32)
+        self.free_pages = room[:self.n_pages].contiguous()
+        self.n_free = (self.n_free + n).clamp(max=self.n_pages)

@@ -542,7 +542,8 @@ sdk_status sdk_chunk_attn(const void* q, int64_t n_tok, int32_t B, int32_t Hq, i
     return SDK_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return SDK_ERR_INVALID_ARG;
   if (bad_pool(pages, n_pages, page_size) || bad_workspace(workspace) ||
-      (int64_t)max_pages * page_size < max_len)
+      (int64_t)max_pages * page_size < max_len ||
+      (int64_t)n_pages * page_size * Hkv > 0xFFFFFFFFll)   // records are counted in 32 bits
     return SDK_ERR_INVALID_ARG;
   if (!dict_k || !dict_v || !block_table || !lens || !cu_q || !aligned(dict_k, 16) ||
       !aligned(dict_v, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(cu_q, 4))

@@ -1,9 +1,15 @@
 // Attention of new tokens over paged codes (sdk_chunk_attn, include/sdk.h).
 //
-// Two kernels: rebuild_kernel writes the context's vectors
+// The form for many rows (few rows over long contexts go by atoms,
+// chunk_atoms.cu): the context's vectors
 //   K_t = sum_j c_tj D_K[i_tj],  V_t = sum_j c_tj D_V[i_tj]
-// once per call as fp16 tiles of 128 tokens in the workspace, and
-// chunk_attn_kernel computes softmax(scale q K^T) V over the tiles.
+// are rebuilt once per call as fp16 tiles of 128 tokens in the workspace, and
+// softmax(scale q K^T) V is computed over the tiles.
+//   chunk_prep_kernel   the plan, the queries as fp16 tiles of packed rows
+//   rebuild_kernel      the tiles of keys and values (short contexts: all of
+//                       this in rebuild_kernel)
+//   chunk_attn_kernel   the attention
+//   chunk_join_kernel   the sums of blocks that several CTAs shared
 #include "chunk_plan.cuh"
 #include "tc_ptx.cuh"
 
@@ -77,9 +83,10 @@ __device__ __forceinline__ void block_tiles(const ChunkParams& p, const ReqPlan&
 // besides (queries in, outputs out, a pipeline filled and drained: 12000
 // cycles against 3000 a tile); a block that sees nothing counts as one, so
 // that its rows are written.
-constexpr int kMaxShares = 160;
 constexpr int kBlockCost = 4;
 __device__ __forceinline__ int block_units(int tiles) { return tiles > 0 ? tiles + kBlockCost : 1; }
+
+constexpr int kMaxShares = 160;    // shares at most (one per SM; chunk_join_kernel's weights)
 
 // One CTA: the running sum of the blocks' units over all requests, every
 // request's first one, and the number of shares: as many as CTAs, but of four
@@ -264,38 +271,36 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
       }
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool bad = false;
-      {
-        auto word = [&](int j) {
-          return __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL);
-        };
-        auto add = [&](float c, const uint4& v) {
-          acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
-          acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
-          acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
-          acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
-          acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
-          acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
-          acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
-          acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
-        };
-        auto atom = [&](uint32_t x) {
-          const uint32_t a = word_idx(x);
-          if (a >= (uint32_t)p.n) bad = true;
-          return a < (uint32_t)p.n ? a : 0u;
-        };
-        auto coef = [&](uint32_t x) { return word_idx(x) < (uint32_t)p.n ? word_coef(x) : 0.0f; };
-        if (TOK == 1) {
-          uint4 v[kAtoms];
+      auto word = [&](int j) {
+        return __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL);
+      };
+      auto add = [&](float c, const uint4& v) {
+        acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
+        acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
+        acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
+        acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
+        acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
+        acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
+        acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
+        acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
+      };
+      auto atom = [&](uint32_t x) {
+        const uint32_t a = word_idx(x);
+        if (a >= (uint32_t)p.n) bad = true;
+        return a < (uint32_t)p.n ? a : 0u;
+      };
+      auto coef = [&](uint32_t x) { return word_idx(x) < (uint32_t)p.n ? word_coef(x) : 0.0f; };
+      if (TOK == 1) {
+        uint4 v[kAtoms];
 #pragma unroll
-          for (int j = 0; j < kAtoms; ++j) v[j] = __ldg(dict + (int64_t)atom(word(j)) * LPR + sub);
+        for (int j = 0; j < kAtoms; ++j) v[j] = __ldg(dict + (int64_t)atom(word(j)) * LPR + sub);
 #pragma unroll
-          for (int j = 0; j < kAtoms; ++j) add(coef(word(j)), v[j]);
-        } else {
+        for (int j = 0; j < kAtoms; ++j) add(coef(word(j)), v[j]);
+      } else {
 #pragma unroll
-          for (int j = 0; j < kAtoms; ++j) {
-            const uint32_t x = word(j);
-            add(coef(x), __ldg(dict + (int64_t)atom(x) * LPR + sub));
-          }
+        for (int j = 0; j < kAtoms; ++j) {
+          const uint32_t x = word(j);
+          add(coef(x), __ldg(dict + (int64_t)atom(x) * LPR + sub));
         }
       }
       // fp16 tiles: 11 significand bits (bf16 would have 8, and its
@@ -340,10 +345,17 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
 // rescaled in TMEM, which is rare); P is 2^7 above its nominal range, so it
 // stays below 2^15 and its smallest fp16 step is 2^-31 of the row's largest
 // term: what 2^18 tokens lose by it is below 2^-13.
-// The CTAs stay, one per SM, and take equal shares of all tiles of all
-// blocks; a block that a share's end cuts leaves partial sums that
-// chunk_join_kernel joins.  (A CTA per block left the SMs idle for 13 % of
-// two rounds at 256 blocks, and long contexts of few rows on few SMs.)
+// A CTA takes a block (256 packed rows of a KV head), or an equal share of all
+// blocks' tiles (chunk_cut says which); a block that a share's end cuts leaves
+// partial sums that chunk_join_kernel joins.
+// 2048 tokens over 32768, 32 heads: 910 us of 1248, 1170 TFLOP/s; the tensor
+// pipe is busy two thirds of a tile's 3000 cycles, the rest is the chain score
+// - maximum - exponentials - P of a row (1800 cycles) that the other tile's
+// products hide in part.  The card is at its power limit there (1000 W at
+// 1.5 to 1.8 GHz), so that fewer idle cycles bring less than they seem to.
+// Tried: a second warpgroup for each tile (half a row a thread) is bound by
+// the exponentials at the same time; half of them on the FMA units instead of
+// a quarter is 2 % slower, none 1 %.
 namespace {
 
 constexpr int kAThreads = 384;     // a warpgroup for each row tile, one of MMA and copy warps
@@ -383,7 +395,8 @@ __device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
 // The whole warp runs the issuing loop, so that its values stay in uniform
 // registers (which the instruction takes its operands from), and the elected
 // lane issues four steps of 16 at a time: with one lane in a branch of its
-// own the issue was the bound (2048 tokens over 32768: 1084 us, so 916 us).
+// own the issue was the bound (this kernel for 2048 tokens over 32768, 32
+// heads: 1084 us, so 916 us).
 // ss: A and B 16 elements (32 bytes) further along K each step; ts: A 8 TMEM
 // columns, B 16 rows of 128 bytes.
 __device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
@@ -1119,7 +1132,7 @@ int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
 // and 20 for every pair that an SM starts on.  32 query and 8 KV heads, one
 // token: 2048 tokens 41 against 60, 8192 tokens 97 against 69, 32768 tokens 256
 // against 116; four tokens over 32768 254 against 185, eight 250 against 282.
-static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q, int max_len,
+static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int max_q, int max_len,
                      int64_t total_len) {
   const int64_t q = max_q < n_tok ? max_q : n_tok, g = Hq / Hkv;
   if (q < 1) return false;
@@ -1163,7 +1176,7 @@ size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n
   const size_t a = chunk_layout(B, blocks, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.ctas,
                                 c.whole)
                        .total;
-  if (!by_atoms(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len)) return a;
+  if (!by_atoms(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len)) return a;
   const size_t b = atoms_workspace_bytes(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
   return a > b ? a : b;
 }
@@ -1214,7 +1227,7 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
                              cudaStream_t stream) {
   p.hdr = reinterpret_cast<WsHeader*>(workspace);
   p.plan = reinterpret_cast<ReqPlan*>(workspace + sizeof(WsHeader));
-  if (by_atoms(p.B, p.n_tok, p.Hq, p.Hkv, p.d, p.n, p.max_q, p.max_len, total_len)) {
+  if (by_atoms(p.B, p.n_tok, p.Hq, p.Hkv, p.d, p.max_q, p.max_len, total_len)) {
     bool taken = false;
     const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
     if (taken) return s;

@@ -93,6 +93,7 @@ CHUNK = dict(q=_at(0), n_tok=7, B=3, Hq=32, Hkv=8, d=128, dk=_at(1), dv=_at(2), 
     (dict(max_len=1281), 1),                   # 20 pages of 64 hold 1280 tokens
     (dict(max_pages=0), 1), (dict(total=-1), 1), (dict(window=-1), 1),
     (dict(window=5, flags=0), 1),              # a window needs the causal order
+    (dict(n_pages=1 << 25, page_size=32, Hkv=8), 1),   # 2^33 records
     (dict(flags=2), 1), (dict(flags=0), 3), (dict(scale=0.0), 1), (dict(scale=float("inf")), 1),
     (dict(scale=float("nan")), 1), (dict(q=None), 1), (dict(q=OFF), 1), (dict(out=None), 1),
     (dict(out=OFF), 1), (dict(lse=OFF, ws_bytes=0), 1), (dict(dk=None), 1), (dict(dv=OFF), 1),

@@ -340,6 +340,9 @@ SHAPES = [
     dict(lens=[20001, 0, 500, 1], new=[3, 0, 2, 1], Hq=12, Hkv=4, n=1001, P=24, d=64),
     dict(lens=[70000, 3], new=[1, 1], Hq=1, Hkv=1, n=32767, P=7),     # one row of a pair
     dict(lens=[1100] * 30, new=[1] * 30, Hq=4, Hkv=2, n=513, d=64),   # many requests
+    dict(lens=[150000], new=[1], Hq=3, Hkv=1, n=2, P=64),             # two atoms
+    dict(lens=[33000, 100], new=[40, 2], Hq=4, Hkv=1, P=32),          # one block shared by all SMs
+    dict(lens=[2500], new=[2500], Hq=32, Hkv=8, n=300, d=64, P=64),   # more blocks than SMs
 ]
 
 
@@ -508,9 +511,11 @@ def test_offsets_past_32_bits():
     assert torch.equal(big[-1, :, -1, 0], k[0]) and torch.equal(big[extra, :, 0, 1], k[1])
 
 
-def test_other_stream_and_repeat():
+@pytest.mark.parametrize("lens,new", [([2500, 300], [4, 200]), ([40000, 300], [2, 1]),
+                                      ([30000, 300], [40, 30])])
+def test_other_stream_and_repeat(lens, new):
     """The same bits on another stream, with a workspace of old contents."""
-    c = Case([2500, 300], [4, 200], seed=9)
+    c = Case(lens, new, seed=9)
     want = c.run()
     ws = c.workspace()
     ws[256:] = 0xFF
@@ -521,6 +526,111 @@ def test_other_stream_and_repeat():
         b = c.run(ws=ws)
     s.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want)
+
+
+@pytest.mark.parametrize("size", [1e-3, 30.0])
+@pytest.mark.parametrize("lens,new", [([900, 300], [50, 1]), ([40000], [1])])
+def test_dictionaries_of_other_norms(size, lens, new):
+    c = Case(lens, new, seed=12)
+    c.dk, c.dv = (c.dk * size).contiguous(), (c.dv * size).contiguous()
+    c.check(scale=1 / math.sqrt(128) / size)
+
+
+@pytest.mark.parametrize("lens,new", [([900, 300], [50, 1]), ([40000], [1])])
+def test_entries_out_of_range_are_recorded(lens, new):
+    """Rebuilt entries, or <q, D_K>, past fp16's range: recorded, and finite."""
+    c = Case(lens, new, seed=13)
+    c.dk, c.dv = (c.dk * 1e6).contiguous(), (c.dv * 1e6).contiguous()
+    ws = c.workspace()
+    assert torch.isfinite(c.run(ws=ws, scale=1e-9)).all() and _status(ws)[0] == 6
+
+
+@pytest.mark.parametrize("kw", SHAPES, ids=lambda k: "%s-%s" % (k["lens"][:4], k["new"][:4]))
+def test_nothing_is_written_behind_the_workspace(kw):
+    c = Case(**kw, seed=14)
+    n = c.workspace().numel()
+    ws = sdk.new_workspace(n + (1 << 20))
+    ws[n:] = 0xA5
+    out = torch.full((c.q.shape[0] + 3, *c.q.shape[1:]), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.run(ws=ws[:n], out=out[1:-2])
+    assert (ws[n:] == 0xA5).all() and (out[0] == 7.0).all() and (out[-2:] == 7.0).all()
+    with pytest.raises(sdk.SdkError, match="SDK_ERR_CAPACITY"):
+        c.run(ws=ws[:(n - 1) // 256 * 256])
+
+
+def test_offsets_that_fall_stay_inside():
+    """cu_q going up and down claims rows many times over: requests are
+    refused where the workspace has no room for them, nothing else is hurt."""
+    c = Case([200] * 40, [10] * 40, Hq=8, Hkv=2, n=500)
+    n = c.workspace().numel()
+    ws = sdk.new_workspace(n + (1 << 20))
+    ws[n:] = 0xA5
+    c.cu = [0 if i % 2 else 10 for i in range(41)]
+    c.run(ws=ws[:n])
+    assert _status(ws)[0] in (3, 6) and (ws[n:] == 0xA5).all()
+    c.cu = [0] + [400 - 10 * (i % 40) for i in range(40)]
+    c.run(ws=ws[:n])
+    assert _status(ws)[0] in (3, 6) and (ws[n:] == 0xA5).all()
+
+
+def test_many_requests():
+    """4096 requests of a few tokens, idle ones among them."""
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 12, (4096,), generator=g).tolist()
+    new = [min(x, 1 + i % 2) if i % 7 else 0 for i, x in enumerate(lens)]
+    Case(lens, new, Hq=2, Hkv=1, d=64, n=100, P=4, cols=3).check()
+
+
+def test_two_calls_at_once():
+    """Two calls on two streams with a workspace each."""
+    a, b = Case([3000], [300], seed=15), Case([30000], [1], seed=16)
+    want = [a.run(), b.run()]
+    ws, streams = [a.workspace(), b.workspace()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.run(ws=ws[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
+
+
+def test_stream_argument():
+    """A call given a stream runs, and makes its outputs, on that stream."""
+    c = Case([700], [5], seed=17)
+    want = c.run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = c.run(stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    r = sdk.sdk_block_tables(_i32([3]), _i32([2]), _i32([1, 0]), _i32([2]), _i32([[0, -1]]), 4, 2,
+                             stream=s)
+    s.synchronize()
+    assert r.slot_map.tolist() == [3, 0] and r.n_free.tolist() == [1]
+
+
+def test_arguments_are_checked():
+    c = Case([20], [2])
+    with pytest.raises(ValueError, match="dtype"):
+        c.run(q=c.q.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        c.run(q=c.q.expand(2, 8, 128)[:, ::2])
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        c.run(q=c.q.cpu())
+    with pytest.raises(ValueError, match="shape"):
+        c.run(out=c.q[:1])
+    with pytest.raises(ValueError, match="cu_q"):
+        sdk.sdk_chunk_attn(c.q, c.dk, c.dv, c.pages, c.table, _i32([20, 20]), _i32([0, 2]), 2, 32)
+    with pytest.raises(sdk.SdkError, match="SDK_ERR_INVALID_ARG"):
+        c.run(window=-1)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.run(max_q=1 << 40)
+    with pytest.raises(ValueError, match="n_new"):
+        sdk.sdk_block_tables(_i32([3]), _i32([2, 2]), _i32([1]), _i32([1]), _i32([[0]]), 4, 2)
+    with pytest.raises(ValueError, match="pages must be"):
+        sdk.sdk_paged_store(c.pages[0], c.table, c.table, torch.zeros(1, device="cuda").long())
 
 
 # ------------------------------------------------------------ all together
