@@ -520,9 +520,10 @@ SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dt
  *   the products in fp16 (fp32 sums), weights per atom with 16 significand
  *   bits; q exactly.  A rebuilt entry beyond +-65504 or NaN is recorded
  *   (SDK_ERR_DEVICE_CHECK) and taken as +-65504 or 0; below 2^-14 it keeps an
- *   absolute error of 2^-25, as the coefficients themselves do.  So is a code
- *   word whose atom is not in the dictionary or, by atoms, whose coefficient
- *   is infinite or NaN, where a row gives it weight; <q, D_K> is exact in
+ *   absolute error of 2^-25, as the coefficients themselves do.  So is, by
+ *   atoms, an infinite or NaN coefficient; a code word whose atom is not in
+ *   the dictionary is recorded and counts as 0.  By atoms, a value's words
+ *   are examined where a row gives its token weight, and <q, D_K> stays in
  *   range for atoms of norms up to 2900.
  * A request whose cu_q, n or len lies outside its bounds is refused:
  *   recorded, its rows are not touched.

@@ -478,8 +478,9 @@ class PagedCodeStore:
         self.n_pages, self.Hkv, self.page_size = n_pages, Hkv, page_size
         self.pages = torch.zeros(n_pages, Hkv, page_size, 2, K_ATOMS, dtype=torch.int32,
                                  device=device)
-        # page 0 on top of the stack
-        self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        # page 0 on top of the stack; one place behind it for what does not fit
+        self._room = torch.arange(n_pages - 1, -2, -1, dtype=torch.int32, device=device)
+        self.free_pages = self._room[:n_pages]
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
 
     def plan(self, lens, n_new, block_table, max_new, workspace=None, stream=None):
@@ -497,7 +498,5 @@ class PagedCodeStore:
         pool's number are dropped (a page was released twice)."""
         n = page_ids.numel()
         at = self.n_free.long() + torch.arange(n, device=self.free_pages.device)
-        room = torch.cat([self.free_pages, self.free_pages.new_empty(n)])
-        room[at] = page_ids.to(torch.int32)
-        self.free_pages = room[:self.n_pages].contiguous()
+        self._room[at.clamp(max=self.n_pages)] = page_ids.to(torch.int32)
         self.n_free = (self.n_free + n).clamp(max=self.n_pages)

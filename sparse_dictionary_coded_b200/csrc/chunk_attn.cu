@@ -1141,6 +1141,10 @@ static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int max_q, in
   double T = (double)B * max_len;
   if (total_len > 0 && total_len < T) T = (double)total_len;
   T *= Hkv;
+  // an atom's sum over a share's tokens has to fit 32 bits with its roundings
+  // (half a unit, 16 words a token), and the pairs fit a grid
+  if (min((double)max_len, T * pairs / num_sms()) > (double)(1 << 24) || all > (double)(1 << 21))
+    return false;
   return 45 + 1.7e-4 * T + 5.5e-5 * T * pairs + 20 * all / num_sms() < 30 + 0.84e-3 * T * (d / 128.0);
 }
 

@@ -698,6 +698,20 @@ def test_serving_steps():
     assert len(set(live)) == len(live)
 
 
+def test_pages_released_twice_are_dropped():
+    """What the stack has no place for is dropped; the stack stays where a
+    captured plan reads it."""
+    store = sdk.PagedCodeStore(6, 1, 4)
+    at = store.free_pages.data_ptr()
+    table = _i32([[-1] * 6])
+    store.plan(_i32([0]), _i32([12]), table, 12)
+    store.release(_i32([0, 1, 2]))
+    assert store.n_free.tolist() == [6] and sorted(store.free_pages.tolist()) == list(range(6))
+    store.release(_i32([0, 1]))
+    assert store.n_free.tolist() == [6] and sorted(store.free_pages.tolist()) == list(range(6))
+    assert store.free_pages.data_ptr() == at
+
+
 def test_captured_step_replays():
     """One step of single tokens captured in a CUDA graph and replayed: the
     lengths advance on the device, and every replay equals the eager step."""
