@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdk.so")
 BINDING = os.path.join(PKG, "_binding.so")
 
-SOURCES = ["api.cu", "chunk_atoms.cu", "chunk_attn.cu", "decode.cu", "decode_static.cu", "encode_simt.cu", "encode_small.cu",
+SOURCES = ["api.cu", "chunk_atoms.cu", "chunk_attn.cu", "chunk_direct.cu", "decode.cu", "decode_static.cu", "encode_simt.cu", "encode_small.cu",
            "encode_tc.cu", "out_tc.cu", "paged.cu", "qd_tc.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -269,59 +269,10 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
           record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x76000000u | (uint32_t)b);
         }
       }
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool bad = false;
-      auto word = [&](int j) {
-        return __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL);
-      };
-      auto add = [&](float c, const uint4& v) {
-        acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
-        acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
-        acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
-        acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
-        acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
-        acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
-        acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
-        acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
-      };
-      auto atom = [&](uint32_t x) {
-        const uint32_t a = word_idx(x);
-        if (a >= (uint32_t)p.n) bad = true;
-        return a < (uint32_t)p.n ? a : 0u;
-      };
-      auto coef = [&](uint32_t x) { return word_idx(x) < (uint32_t)p.n ? word_coef(x) : 0.0f; };
-      if (TOK == 1) {
-        uint4 v[kAtoms];
-#pragma unroll
-        for (int j = 0; j < kAtoms; ++j) v[j] = __ldg(dict + (int64_t)atom(word(j)) * LPR + sub);
-#pragma unroll
-        for (int j = 0; j < kAtoms; ++j) add(coef(word(j)), v[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kAtoms; ++j) {
-          const uint32_t x = word(j);
-          add(coef(x), __ldg(dict + (int64_t)atom(x) * LPR + sub));
-        }
-      }
-      // fp16 tiles: 11 significand bits (bf16 would have 8, and its
-      // rounding of K, V and the probabilities would double the output's
-      // error), the range the coefficients themselves have
-      __half2 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x0 = acc[2 * i], x1 = acc[2 * i + 1];
-        if (!(fabsf(x0) <= 65504.0f)) {
-          bad = true;
-          x0 = x0 != x0 ? 0.0f : copysignf(65504.0f, x0);
-        }
-        if (!(fabsf(x1) <= 65504.0f)) {
-          bad = true;
-          x1 = x1 != x1 ? 0.0f : copysignf(65504.0f, x1);
-        }
-        o[i] = __floats2half2_rn(x0, x1);
-      }
+      const uint4 y = rebuild_piece<D, TOK == 1>(p, dict, w, rec, sub, &bad);
       if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
-      *reinterpret_cast<uint4*>(dst + tile_off(r, sub)) = *reinterpret_cast<const uint4*>(o);
+      *reinterpret_cast<uint4*>(dst + tile_off(r, sub)) = y;
     }
   }
   // done only when chunk_prep_kernel is: the next kernel waits for this one alone
@@ -1174,6 +1125,9 @@ static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
 
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len) {
+  if (!by_atoms(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len) &&
+      direct_fits(B, n_tok, Hq / Hkv, Hkv, max_q, max_len))
+    return direct_workspace_bytes(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len);
   const int64_t q = max_q < n_tok ? max_q : n_tok;
   const int64_t blocks = cap_blocks(B, n_tok, Hq / Hkv, (int)q);
   const ChunkCut c = chunk_cut(blocks, Hkv, max_len);
@@ -1235,6 +1189,8 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
     bool taken = false;
     const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
     if (taken) return s;
+  } else if (direct_fits(p.B, p.n_tok, p.g, p.Hkv, p.max_q, p.max_len)) {
+    return launch_chunk_direct(p, total_len, workspace, stream);
   }
   const int64_t blocks = cap_blocks(p.B, p.n_tok, p.g, p.max_q);
   p.cap_work = blocks;

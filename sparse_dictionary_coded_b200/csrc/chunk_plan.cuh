@@ -166,6 +166,66 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Lane `sub` of the D / 8 that rebuild record `rec` of the warp: its eight
+// entries of sum_j c_j dict[i_j] as fp16.  w: the lane's 16 / (D / 8) code
+// words; ALL: all 16 atoms' rows in flight.  bad: an atom not in the
+// dictionary (it counts as 0) or an entry out of range.
+template <int D, bool ALL>
+__device__ __forceinline__ uint4 rebuild_piece(const ChunkParams& p, const uint4* dict,
+                                               const uint32_t (&w)[128 / D], int rec, int sub,
+                                               bool* bad) {
+  constexpr int LPR = D / 8, WPL = 16 / LPR;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  auto word = [&](int j) { return __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL); };
+  auto add = [&](float c, const uint4& v) {
+    acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
+    acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
+    acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
+    acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
+    acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
+    acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
+    acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
+    acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
+  };
+  auto atom = [&](uint32_t x) {
+    const uint32_t a = word_idx(x);
+    if (a >= (uint32_t)p.n) *bad = true;
+    return a < (uint32_t)p.n ? a : 0u;
+  };
+  auto coef = [&](uint32_t x) { return word_idx(x) < (uint32_t)p.n ? word_coef(x) : 0.0f; };
+  if (ALL) {
+    uint4 v[kAtoms];
+#pragma unroll
+    for (int j = 0; j < kAtoms; ++j) v[j] = __ldg(dict + (int64_t)atom(word(j)) * LPR + sub);
+#pragma unroll
+    for (int j = 0; j < kAtoms; ++j) add(coef(word(j)), v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kAtoms; ++j) {
+      const uint32_t x = word(j);
+      add(coef(x), __ldg(dict + (int64_t)atom(x) * LPR + sub));
+    }
+  }
+  // fp16: 11 significand bits (bf16 would have 8, and its rounding of K, V
+  // and the probabilities would double the output's error), the range the
+  // coefficients themselves have
+  __half2 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0 = acc[2 * i], x1 = acc[2 * i + 1];
+    if (!(fabsf(x0) <= 65504.0f)) {
+      *bad = true;
+      x0 = x0 != x0 ? 0.0f : copysignf(65504.0f, x0);
+    }
+    if (!(fabsf(x1) <= 65504.0f)) {
+      *bad = true;
+      x1 = x1 != x1 ? 0.0f : copysignf(65504.0f, x1);
+    }
+    o[i] = __floats2half2_rn(x0, x1);
+  }
+  return *reinterpret_cast<const uint4*>(o);
+}
+
 // Launches a kernel that may start while its predecessor in the stream
 // drains; the kernel itself waits (pdl_wait) before it touches global memory.
 template <class... KArgs, class... Args>

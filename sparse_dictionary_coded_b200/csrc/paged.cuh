@@ -84,11 +84,16 @@ sdk_status launch_paged_store(const StoreParams& p, cudaStream_t stream);
 // total_len as the caller's (0: B * max_len)
 sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
                              cudaStream_t stream);
-// the two forms' parts (chunk_attn.cu, chunk_atoms.cu)
+// the other two forms (chunk_atoms.cu, chunk_direct.cu)
 size_t atoms_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len);
 sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
                               cudaStream_t stream, bool* taken);
+bool direct_fits(int B, int64_t n_tok, int g, int Hkv, int max_q, int max_len);
+size_t direct_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int max_q, int max_len,
+                              int64_t total_len);
+sdk_status launch_chunk_direct(ChunkParams p, int64_t total_len, char* workspace,
+                               cudaStream_t stream);
 // total bytes of the chunk attention's workspace
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len);
