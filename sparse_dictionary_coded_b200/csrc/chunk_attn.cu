@@ -1126,7 +1126,7 @@ static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len) {
   if (!by_atoms(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len) &&
-      direct_fits(B, n_tok, Hq / Hkv, Hkv, max_q, max_len))
+      direct_fits(B, n_tok, Hq / Hkv, max_q, max_len))
     return direct_workspace_bytes(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len);
   const int64_t q = max_q < n_tok ? max_q : n_tok;
   const int64_t blocks = cap_blocks(B, n_tok, Hq / Hkv, (int)q);
@@ -1189,7 +1189,7 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
     bool taken = false;
     const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
     if (taken) return s;
-  } else if (direct_fits(p.B, p.n_tok, p.g, p.Hkv, p.max_q, p.max_len)) {
+  } else if (direct_fits(p.B, p.n_tok, p.g, p.max_q, p.max_len)) {
     return launch_chunk_direct(p, total_len, workspace, stream);
   }
   const int64_t blocks = cap_blocks(p.B, p.n_tok, p.g, p.max_q);

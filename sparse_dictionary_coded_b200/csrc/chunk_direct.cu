@@ -4,8 +4,8 @@
 // as fp16 in shared memory and attends to them at once, with a running
 // maximum and sum per row, so that nothing but the partial sums of contexts
 // that several CTAs share goes through the workspace.
-//   chunk_direct_kernel       shares of all contexts
-//   chunk_direct_join_kernel  the sums of contexts that several shares hold
+//   chunk_direct_kernel       all contexts, in parts of equal length
+//   chunk_direct_join_kernel  the sums of contexts in several parts
 // What counts here is the chain of dependent loads: lengths, page, code words,
 // atoms' rows (16 in flight a lane).
 #include "chunk_plan.cuh"
@@ -18,26 +18,27 @@ namespace {
 constexpr int kDirThreads = 256, kDirWarps = kDirThreads / 32;
 constexpr int kUnit = 16;          // tokens of a unit of work
 constexpr int kStep = 32;          // tokens rebuilt and attended to at a time
-constexpr int kJoinGroups = 4;     // warps that share a row's parts when joining
+constexpr int kMaxParts = 512;     // CTAs, and parts of a context
+constexpr int kJoinRows = 8;       // blocks that share a context's rows when joining, at least
 constexpr float kUp = 14.0f;       // log2 of P's offset: its smallest fp16 step is 2^-38 of the largest term
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// What share c of the work starts with, left for the join.
-struct Cut {
-  int64_t u0;          // its first unit
-  int64_t lo, hi;      // the units of the context that unit belongs to
-  int row0, rows, h;
+// A context of one KV head in several parts, left for the join.
+struct Split {
+  int row0, rows, h, parts, slot;
 };
 
 struct DirectLayout {
-  size_t cuts, ml, po, total;
+  size_t splits, ml, po, total;
 };
 
-DirectLayout direct_layout(int B, int rows, int d, int ctas) {
+DirectLayout direct_layout(int rows, int d, int ctas) {
   DirectLayout l;
-  l.cuts = up256(sizeof(WsHeader) + sizeof(ReqPlan));
-  l.ml = up256(l.cuts + (size_t)ctas * sizeof(Cut));
+  l.splits = up256(sizeof(WsHeader) + sizeof(ReqPlan));
+  // a context in parts of S units has at most 2 u / S, so all of them at
+  // most twice as many parts as there are CTAs, and half as many contexts
+  l.ml = up256(l.splits + (size_t)ctas * sizeof(Split));
   l.po = up256(l.ml + (size_t)2 * ctas * rows * 8);
   l.total = up256(l.po + (size_t)2 * ctas * rows * d * 4);
   return l;
@@ -45,12 +46,13 @@ DirectLayout direct_layout(int B, int rows, int d, int ctas) {
 
 int pad_rows(int64_t rows) { return rows <= 16 ? 16 : 32; }
 
-// Shares at most: two CTAs per SM, or one for every unit there can be.
+// Two CTAs per SM, or one for every unit there can be.
 int direct_ctas(int B, int Hkv, int max_len, int64_t total_len) {
   int64_t units = (int64_t)B * (max_len / kUnit + 2);
   if (total_len > 0 && total_len / kUnit + 2 * (int64_t)B < units) units = total_len / kUnit + 2 * (int64_t)B;
   units *= Hkv;
-  return (int)(units < 2 * num_sms() ? units : 2 * num_sms());
+  const int most = 2 * num_sms() < kMaxParts ? 2 * num_sms() : kMaxParts;
+  return (int)(units < most ? units : most);
 }
 
 // Four 8x8 matrices of halves from shared memory, rows at the lanes' addresses.
@@ -75,11 +77,12 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 
 }  // namespace
 
-// Every CTA scans the requests itself (at most one per thread) and takes an
-// equal share of the units of 16 tokens of all (request, KV head) contexts, in
-// that order; a share's segments are attended to one after the other.  The
-// products are small (32 tokens and 16 or 32 rows at a time), so the warps'
-// own matrix instructions do them; P and the sums as in chunk_attn.cu.
+// Every CTA looks over the requests itself (at most one per thread): the
+// contexts are cut into parts of S units of 16 tokens, S the smallest length
+// that leaves no more parts than CTAs (shares of exactly equal length made
+// some CTAs walk the chain of loads twice: drafts of eight requests 24.6 us).
+// The products are small (32 tokens and 16 or 32 rows at a time), so the
+// warps' own matrix instructions do them; P and the sums as in chunk_attn.cu.
 template <int D, int MT>
 __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParams p) {
   constexpr int kR = MT * 16;          // rows, padded
@@ -96,88 +99,103 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
   __shared__ __align__(16) __half s_p[kR * (kStep + 8)];
   __shared__ float s_s[kR * (kStep + 1)];
   __shared__ float s_c[kR], s_f[kR], s_m[kR], s_l[kR];
-  __shared__ int64_t s_work[kDirThreads + 1];
   __shared__ int4 s_req[kDirThreads];             // row0, n, len, first token
-  __shared__ int64_t s_warp[32];
-  __shared__ int s_units;
+  __shared__ int s_units[kDirThreads], s_tiles[kDirThreads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
-  // ---- the plan.  Tiles of 128 tokens are what the caller's bound on the
-  // lengths is held against, as in the other form.
-  if (tid == 0) {
-    s_units = 0;
-    s_work[0] = 0;
-  }
-  unsigned err = 0;
-  ReqPlan rq = {};
-  int units = 0;
+  // ---- the plan, by every warp for itself
   if (tid < p.B) {
-    rq = check_request(p, tid, &err);
+    unsigned err;
+    const ReqPlan rq = check_request(p, tid, &err);
+    int lo = 0, units = 0;
     if (rq.n > 0) {
       // the first token any row sees, rounded down to a unit
       const int seen = p.window > 0 ? max(rq.len - rq.n - p.window + 1, 0) : 0;
-      rq.lo = min(seen, rq.len) / kUnit * kUnit;
-      units = max((rq.len - rq.lo + kUnit - 1) / kUnit, 1);
+      lo = min(seen, rq.len) / kUnit * kUnit;
+      units = max((rq.len - lo + kUnit - 1) / kUnit, 1);
     }
-  }
-  int64_t both;
-  const int64_t upto =
-      block_scan64(((int64_t)rq.ntiles << 32) + units, s_warp, &both);
-  if (tid < p.B) {
-    if (rq.n > 0 && (upto >> 32) > p.cap_tiles) {
-      err = SDK_ERR_CAPACITY;
-      rq.n = 0;
-    } else if (units > 0) {
-      atomicMax(&s_units, (int)(uint32_t)upto);
-    }
-    s_work[tid + 1] = (int64_t)(uint32_t)upto * p.Hkv;
-    s_req[tid] = make_int4(rq.row0, rq.n, rq.len, rq.lo);
+    s_req[tid] = make_int4(rq.row0, rq.n, rq.len, lo);
+    s_units[tid] = units;
+    s_tiles[tid] = rq.ntiles;
     if (err && blockIdx.x == 0) record_error(p.hdr, err, 0x75000000u | (uint32_t)tid);
   }
   __syncthreads();
-  const int64_t U = (int64_t)s_units * p.Hkv;
-  const int N = (int)min(U, (int64_t)gridDim.x), me = (int)blockIdx.x;
-  if (me == 0 && tid == 0) {
-    p.plan[0].work0 = U;
-    p.plan[0].npair = N;
-  }
-  if (me >= N) return;
-  int64_t u = U * me / N;
-  const int64_t u_end = U * (me + 1) / N;
-  int b = 0;
-  {
-    int hi = p.B;
-    while (hi - b > 1) {
-      const int mid = (b + hi) >> 1;
-      if (s_work[mid] <= u) b = mid; else hi = mid;
+  auto sum_of = [&](auto f) {          // of all requests
+    int v = 0;
+    for (int r = lane; r < p.B; r += 32) v += f(r);
+    return __reduce_add_sync(0xffffffffu, v);
+  };
+  // tiles of 128 tokens are what the caller's bound on the lengths is held
+  // against, as in the other form
+  if (sum_of([&](int r) { return s_tiles[r]; }) > p.cap_tiles) {
+    __syncthreads();
+    if (tid == 0) {
+      int64_t tiles = 0;
+      for (int r = 0; r < p.B; ++r) {
+        tiles += s_tiles[r];
+        if (tiles > p.cap_tiles && s_units[r] > 0) {
+          s_units[r] = 0;
+          if (blockIdx.x == 0) record_error(p.hdr, SDK_ERR_CAPACITY, 0x75000000u | (uint32_t)r);
+        }
+      }
     }
+    __syncthreads();
+  }
+  const int U = sum_of([&](int r) { return s_units[r]; });       // per KV head
+  const int room = max((int)gridDim.x / p.Hkv, 1);               // parts per KV head
+  int S = max((U + room - 1) / room, 1), items;
+  auto parts_of = [&](int r) { return (s_units[r] + S - 1) / S; };
+  for (int i = 0;; ++i) {
+    items = sum_of(parts_of);
+    if (items <= room || i == 8) break;            // (more requests than CTAs: several parts each)
+    S += (S + 7) / 8;
   }
 
+  if (blockIdx.x == 0 && warp == 0) {
+    const int splits = sum_of([&](int r) { return parts_of(r) > 1 ? 1 : 0; });
+    if (lane == 0) p.plan[0].npair = splits * p.Hkv;
+  }
   const int rec = lane / LPR, sub = lane % LPR, kv = rec & 1;
   const uint4* dict = reinterpret_cast<const uint4*>(kv ? p.dv : p.dk);
   int buf = 0;
 #pragma unroll 1
-  for (bool first = true; u < u_end; first = false) {
-    while (s_work[b + 1] <= u) ++b;
+  for (int64_t item = blockIdx.x; item < (int64_t)items * p.Hkv; item += gridDim.x) {
+    // part `part` of request b's context, for KV head h
+    const int h = (int)(item % p.Hkv);
+    int part = (int)(item / p.Hkv), b = 0, parts = 0, before = 0, split = 0;   // split parts, contexts before b's
+    for (int r0 = 0;; r0 += 32) {
+      const int mine = r0 + lane < p.B ? parts_of(r0 + lane) : 0;
+      int upto = mine;
+#pragma unroll
+      for (int e = 1; e < 32; e <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, e);
+        if (lane >= e) upto += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, upto > part);
+      const int at = past ? __ffs(past) - 1 : 32;
+      before += __reduce_add_sync(0xffffffffu, lane < at && mine > 1 ? mine : 0);
+      split += __popc(__ballot_sync(0xffffffffu, lane < at && mine > 1));
+      if (past) {
+        b = r0 + at;
+        parts = __shfl_sync(0xffffffffu, mine, at);
+        part -= __shfl_sync(0xffffffffu, upto, at) - parts;
+        break;
+      }
+      part -= __shfl_sync(0xffffffffu, upto, 31);
+    }
     const int4 r4 = s_req[b];
     const int row0 = r4.x, n = r4.y, len = r4.z, rows = n * p.g;
-    const int64_t w0 = s_work[b];
-    const int per = (int)((uint32_t)((s_work[b + 1] - w0) / p.Hkv));
-    const int rel = (int)(u - w0), h = rel / per, ui = rel - h * per;
-    const int cnt = (int)min((int64_t)(per - ui), u_end - u);
-    const int t_begin = r4.w + ui * kUnit, t_end = min(len, t_begin + cnt * kUnit);
-    // partial sums: of the share's first segment or of its last
-    const int slot = cnt < per ? 2 * me + (first ? 0 : 1) : -1;
-    if (first && tid == 0) {
-      Cut cut;
-      cut.u0 = u;
-      cut.lo = u - ui;
-      cut.hi = cut.lo + per;
-      cut.row0 = row0;
-      cut.rows = rows;
-      cut.h = h;
-      reinterpret_cast<Cut*>(p.cuts)[me] = cut;
+    const int t_begin = r4.w + part * S * kUnit, t_end = min(len, t_begin + S * kUnit);
+    const int slot = parts > 1 ? before * p.Hkv + h * parts + part : -1;
+    if (parts > 1 && part == 0 && tid == 0) {
+      Split c;
+      c.row0 = row0;
+      c.rows = rows;
+      c.h = h;
+      c.parts = parts;
+      c.slot = slot;
+      reinterpret_cast<Split*>(p.cuts)[split * p.Hkv + h] = c;
     }
     // code words of the step at t0: the warp's tokens t0 + warp TPS, and so on
     uint32_t w[NU][WPL];
@@ -371,94 +389,103 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
             p.lse[row] = ls > 0.0f || ls != ls ? (s_m[r] + log2f(ls)) * 0.69314718f : -INFINITY;
         }
       }
-    u += cnt;
   }
 }
 
-// Joins the partial sums of the contexts that several shares hold, in the
-// shares' order: share c stands for the context that its first unit lies
-// inside of, if that is the first cut there.  Four warps share a row's parts,
-// a lane takes D / 32 dims.
+// Joins the partial sums of contexts in several parts, in the parts' order.  A
+// block takes every gridDim.y-th row; of few parts all its rows at once, of
+// many (a head's context of 8192 tokens has 296) one after the other, with
+// more warps to share the parts.  A lane takes D / 32 dims.
 template <int D, int MT>
 __global__ void __launch_bounds__(kDirThreads) chunk_direct_join_kernel(ChunkParams p) {
-  constexpr int kR = MT * 16, E = D / 32, kRowsBlock = kDirWarps / kJoinGroups;
+  constexpr int kR = MT * 16, E = D / 32, kMost = (kR + kJoinRows - 1) / kJoinRows;
   __shared__ float s_o[kDirWarps][D];
+  __shared__ float s_w[kMost][kMaxParts];
   pdl_wait();
-  const Cut* cuts = reinterpret_cast<const Cut*>(p.cuts);
-  const int c = (int)blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Cut cut = cuts[c];                         // (of a share that is not there: not used)
-  const int64_t before = cuts[c - 1].u0, U = p.plan[0].work0;
-  const int shares = p.plan[0].npair;
-  if (c >= shares || cut.u0 == cut.lo || before > cut.lo) return;   // no cut, or an earlier one
-  if ((int)blockIdx.y * kRowsBlock >= cut.rows) return;
-  const int grp = warp % kJoinGroups, r = blockIdx.y * kRowsBlock + warp / kJoinGroups;
-  const bool live = r < cut.rows;
-  // share c - 1 ends with its part, the shares c .. last start with theirs
-  const int slot0 = 2 * (c - 1) + (before < cut.lo ? 1 : 0);
-  const int last = (int)((cut.hi * shares - 1) / U), parts = last - c + 2;
-  auto at = [&](int s) { return (int64_t)(s == 0 ? slot0 : 2 * (c - 1 + s)) * kR + r; };
-  float m = -INFINITY, z = 0.0f, o[E] = {};
-  if (live) {
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_ml[at(s)].x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Split c = reinterpret_cast<const Split*>(p.cuts)[blockIdx.x];
+  if ((int)blockIdx.x >= p.plan[0].npair) return;   // (what is read there is not used)
+  const int parts = c.parts;
+  const int y = (int)blockIdx.y, dy = (int)gridDim.y;
+  if (y >= c.rows) return;
+  const int mine = (c.rows - y + dy - 1) / dy;   // rows of the block
+  const int at_once = parts > 32 ? 1 : mine > 2 ? min(4, kMost) : mine;
+  const int i = warp % at_once, grp = warp / at_once, groups = kDirWarps / at_once;
+#pragma unroll 1
+  for (int i0 = 0; i0 < mine; i0 += at_once) {
+    const int r = y + (i0 + i) * dy;
+    const bool live = i0 + i < mine;
+    auto at = [&](int s) { return (int64_t)(c.slot + s) * kR + r; };
+    float m = -INFINITY, z = 0.0f, o[E] = {};
+    if (live) {
+      // every warp of the row finds the weights (the same ones)
+      float* w = s_w[i];
+#pragma unroll 1
+      for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_ml[at(s)].x);
 #pragma unroll
-    for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
-    // what saw nothing has no weight (its sums are zero)
-    auto weight = [&](const float2& ml) { return ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ex2(ml.x - m); };
-    for (int s = lane; s < parts; s += 32) {
-      const float2 ml = p.part_ml[at(s)];
-      z = fmaf(ml.y, weight(ml), z);
+      for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+#pragma unroll 1
+      for (int s = lane; s < parts; s += 32) {
+        const float2 ml = p.part_ml[at(s)];
+        // what saw nothing has no weight (its sums are zero)
+        const float f = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ex2(ml.x - m);
+        w[s] = f;
+        z = fmaf(ml.y, f, z);
+      }
+#pragma unroll
+      for (int e = 16; e > 0; e >>= 1) z += __shfl_xor_sync(0xffffffffu, z, e);
+      __syncwarp();
+#pragma unroll 8
+      for (int s = grp; s < parts; s += groups) {
+        const float f = w[s];
+        const float* src = p.part_o + at(s) * D + lane * E;
+#pragma unroll
+        for (int k = 0; k < E; ++k) o[k] = fmaf(src[k], f, o[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = o[k];
     }
+    __syncthreads();
+    if (live && grp == 0) {
+      for (int k = 1; k < groups; ++k)
 #pragma unroll
-    for (int e = 16; e > 0; e >>= 1) z += __shfl_xor_sync(0xffffffffu, z, e);
-#pragma unroll 4
-    for (int s = grp; s < parts; s += kJoinGroups) {
-      const float f = weight(p.part_ml[at(s)]);
-      const float* src = p.part_o + at(s) * D + lane * E;
+        for (int e = 0; e < E; ++e) o[e] += s_o[warp + k * at_once][lane * E + e];
+      const int tok = r / p.g;
+      const int64_t row = (int64_t)(c.row0 + tok) * p.Hq + c.h * p.g + (r - tok * p.g);
+      const float inv = z > 0.0f || z != z ? 1.0f / z : 0.0f;
 #pragma unroll
-      for (int k = 0; k < E; ++k) o[k] = fmaf(src[k], f, o[k]);
+      for (int k = 0; k < E; k += 2)
+        *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + lane * E + k) =
+            __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv);
+      if (p.lse != nullptr && lane == 0)
+        p.lse[row] = z > 0.0f || z != z ? (m + log2f(z)) * 0.69314718f : -INFINITY;
     }
-#pragma unroll
-    for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = o[k];
+    __syncthreads();
   }
-  __syncthreads();
-  if (!live || grp > 0) return;
-#pragma unroll
-  for (int i = 1; i < kJoinGroups; ++i)
-#pragma unroll
-    for (int k = 0; k < E; ++k) o[k] += s_o[warp + i][lane * E + k];
-  const int tok = r / p.g;
-  const int64_t row = (int64_t)(cut.row0 + tok) * p.Hq + cut.h * p.g + (r - tok * p.g);
-  const float inv = z > 0.0f || z != z ? 1.0f / z : 0.0f;
-#pragma unroll
-  for (int k = 0; k < E; k += 2)
-    *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + lane * E + k) =
-        __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[row] = z > 0.0f || z != z ? (m + log2f(z)) * 0.69314718f : -INFINITY;
 }
 
 // At most a thread per request, 32 rows per request and KV head, and counts
 // of units that fit 32 bits.
-bool direct_fits(int B, int64_t n_tok, int g, int Hkv, int max_q, int max_len) {
+bool direct_fits(int B, int64_t n_tok, int g, int max_q, int max_len) {
   const int64_t q = max_q < n_tok ? max_q : n_tok;
-  return B <= kDirThreads && q * g <= 32 && max_len <= 1 << 20 && (int64_t)Hkv * max_len <= 1 << 30;
+  return B <= kDirThreads && q * g <= 32 && max_len <= 1 << 20;
 }
 
 size_t direct_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int max_q, int max_len,
                               int64_t total_len) {
   const int64_t q = max_q < n_tok ? max_q : n_tok;
-  return direct_layout(B, pad_rows(q * (Hq / Hkv)), d, direct_ctas(B, Hkv, max_len, total_len)).total;
+  return direct_layout(pad_rows(q * (Hq / Hkv)), d, direct_ctas(B, Hkv, max_len, total_len)).total;
 }
 
 template <int D, int MT>
 static sdk_status launch_direct_d(const ChunkParams& p, cudaStream_t stream) {
   chunk_direct_kernel<D, MT><<<(unsigned)p.ctas, kDirThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
-  const int rows = p.max_q * p.g, each = kDirWarps / kJoinGroups;
-  if (p.ctas > 1 &&
-      launch_after(chunk_direct_join_kernel<D, MT>,
-                   dim3((unsigned)(p.ctas - 1), (unsigned)((rows + each - 1) / each)), kDirThreads, 0,
-                   stream, p) != cudaSuccess)
+  // contexts in several parts: half as many as parts
+  const int rows = p.max_q * p.g, most = min(p.ctas, p.B * p.Hkv);
+  const int y = min(rows, max(kJoinRows, 4 * num_sms() / most));
+  if (p.ctas > 1 && launch_after(chunk_direct_join_kernel<D, MT>, dim3((unsigned)most, (unsigned)y),
+                                 kDirThreads, 0, stream, p) != cudaSuccess)
     return SDK_ERR_CUDA;
   return SDK_OK;
 }
@@ -467,8 +494,8 @@ sdk_status launch_chunk_direct(ChunkParams p, int64_t total_len, char* workspace
                                cudaStream_t stream) {
   const int rows = pad_rows((int64_t)p.max_q * p.g);
   p.ctas = direct_ctas(p.B, p.Hkv, p.max_len, total_len);
-  const DirectLayout l = direct_layout(p.B, rows, p.d, p.ctas);
-  p.cuts = workspace + l.cuts;
+  const DirectLayout l = direct_layout(rows, p.d, p.ctas);
+  p.cuts = workspace + l.splits;
   p.part_ml = reinterpret_cast<float2*>(workspace + l.ml);
   p.part_o = reinterpret_cast<float*>(workspace + l.po);
   if (p.d == 128) return rows > 16 ? launch_direct_d<128, 2>(p, stream) : launch_direct_d<128, 1>(p, stream);
