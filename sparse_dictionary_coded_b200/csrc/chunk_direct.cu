@@ -144,9 +144,13 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
   }
   const int U = sum_of([&](int r) { return s_units[r]; });       // per KV head
   const int room = max((int)gridDim.x / p.Hkv, 1);               // parts per KV head
-  int S = max((U + room - 1) / room, 1), items;
-  auto parts_of = [&](int r) { return (s_units[r] + S - 1) / S; };
+  int S = max((int)((uint32_t)(U + room - 1) / (uint32_t)room), 1), items;
+  float per_s;
+  // ceil(units / S); exact, the quotient is half a unit off whole numbers and
+  // units are at most 2^16
+  auto parts_of = [&](int r) { return (int)(((float)(s_units[r] + S) - 0.5f) * per_s); };
   for (int i = 0;; ++i) {
+    per_s = __frcp_rn((float)S);
     items = sum_of(parts_of);
     if (items <= room || i == 8) break;            // (more requests than CTAs: several parts each)
     S += (S + 7) / 8;
@@ -160,10 +164,10 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
   const uint4* dict = reinterpret_cast<const uint4*>(kv ? p.dv : p.dk);
   int buf = 0;
 #pragma unroll 1
-  for (int64_t item = blockIdx.x; item < (int64_t)items * p.Hkv; item += gridDim.x) {
+  for (uint32_t item = blockIdx.x; item < (uint32_t)(items * p.Hkv); item += gridDim.x) {
     // part `part` of request b's context, for KV head h
-    const int h = (int)(item % p.Hkv);
-    int part = (int)(item / p.Hkv), b = 0, parts = 0, before = 0, split = 0;   // split parts, contexts before b's
+    const int h = (int)(item % (uint32_t)p.Hkv);
+    int part = (int)(item / (uint32_t)p.Hkv), b = 0, parts = 0, before = 0, split = 0;   // split parts, contexts before b's
     for (int r0 = 0;; r0 += 32) {
       const int mine = r0 + lane < p.B ? parts_of(r0 + lane) : 0;
       int upto = mine;
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
 // more warps to share the parts.  A lane takes D / 32 dims.
 template <int D, int MT>
 __global__ void __launch_bounds__(kDirThreads) chunk_direct_join_kernel(ChunkParams p) {
-  constexpr int kR = MT * 16, E = D / 32, kMost = (kR + kJoinRows - 1) / kJoinRows;
+  constexpr int kR = MT * 16, E = D / 32, kMost = (kR + kJoinRows - 1) / kJoinRows, kPre = 4;
   __shared__ float s_o[kDirWarps][D];
   __shared__ float s_w[kMost][kMaxParts];
   pdl_wait();
@@ -418,6 +422,14 @@ __global__ void __launch_bounds__(kDirThreads) chunk_direct_join_kernel(ChunkPar
     auto at = [&](int s) { return (int64_t)(c.slot + s) * kR + r; };
     float m = -INFINITY, z = 0.0f, o[E] = {};
     if (live) {
+      // the warp's first sums are on their way while the weights are found
+      float x[kPre][E];
+#pragma unroll
+      for (int j = 0; j < kPre; ++j)
+        if (grp + j * groups < parts)
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            x[j][k] = p.part_o[at(grp + j * groups) * D + lane * E + k];
       // every warp of the row finds the weights (the same ones)
       float* w = s_w[i];
 #pragma unroll 1
@@ -435,8 +447,13 @@ __global__ void __launch_bounds__(kDirThreads) chunk_direct_join_kernel(ChunkPar
 #pragma unroll
       for (int e = 16; e > 0; e >>= 1) z += __shfl_xor_sync(0xffffffffu, z, e);
       __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kPre; ++j)
+        if (grp + j * groups < parts)
+#pragma unroll
+          for (int k = 0; k < E; ++k) o[k] = fmaf(x[j][k], w[grp + j * groups], o[k]);
 #pragma unroll 8
-      for (int s = grp; s < parts; s += groups) {
+      for (int s = grp + kPre * groups; s < parts; s += groups) {
         const float f = w[s];
         const float* src = p.part_o + at(s) * D + lane * E;
 #pragma unroll
