@@ -511,11 +511,13 @@ SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dt
  * Limits: B <= SDK_MAX_REQUESTS, Hq % Hkv == 0, head_dim 64 or 128, scale >
  *   0, n_tok * Hq < 2^31, max_len <= 2^30, max_pages * page_size >= max_len,
  *   n_pages * page_size * Hkv < 2^32.
- * Two forms, by sizes: many rows attend over vectors that are rebuilt once
- *   per call in the workspace (128-token tiles, tensor cores); few rows over
- *   long contexts go by atoms (scores from <q, D_K>, values through weights
- *   per atom).  Results of one form do not depend on the other requests'
- *   contents, but their last bits may on how the batch cuts the contexts.
+ * Three forms, by sizes: many rows attend over vectors that are rebuilt once
+ *   per call in the workspace (128-token tiles, tensor cores); up to 32 rows
+ *   per request and KV head over short contexts go in one pass; few rows
+ *   over long contexts go by atoms (scores from <q, D_K>, values through
+ *   weights per atom).  Results of one form do not depend on the other
+ *   requests' contents, but their last bits may on how the batch cuts the
+ *   contexts.
  * Arithmetic: rebuilt vectors and probabilities (by atoms: <q, D_K>) enter
  *   the products in fp16 (fp32 sums), weights per atom with 16 significand
  *   bits; q exactly.  A rebuilt entry beyond +-65504 or NaN is recorded

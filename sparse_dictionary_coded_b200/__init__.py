@@ -366,8 +366,8 @@ def sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size,
     [B, max_pages]; max_new: rows of the slot map (a bound on the step's
     tokens).  n_pages: pages of the pool (default: the length of
     free_pages, which may hold fewer entries than the pool has pages).
-    Returns BlockTables; requests that do not fit are refused and recorded
-    in the workspace (include/sdk.h)."""
+    Returns BlockTables, its new tensors in one buffer; requests that do not
+    fit are refused and recorded in the workspace (include/sdk.h)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size, max_new,

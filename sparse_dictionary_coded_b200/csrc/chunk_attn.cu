@@ -1,13 +1,13 @@
 // Attention of new tokens over paged codes (sdk_chunk_attn, include/sdk.h).
 //
-// The form for many rows (few rows over long contexts go by atoms,
-// chunk_atoms.cu): the context's vectors
+// The form for many rows (few rows over short contexts go in one pass,
+// chunk_direct.cu, over long ones by atoms, chunk_atoms.cu): the context's vectors
 //   K_t = sum_j c_tj D_K[i_tj],  V_t = sum_j c_tj D_V[i_tj]
 // are rebuilt once per call as fp16 tiles of 128 tokens in the workspace, and
 // softmax(scale q K^T) V is computed over the tiles.
 //   chunk_prep_kernel   the plan, the queries as fp16 tiles of packed rows
-//   rebuild_kernel      the tiles of keys and values (short contexts: all of
-//                       this in rebuild_kernel)
+//   rebuild_kernel      the tiles of keys and values (few tokens and rows: with
+//                       the plan and the queries)
 //   chunk_attn_kernel   the attention
 //   chunk_join_kernel   the sums of blocks that several CTAs shared
 #include "chunk_plan.cuh"
@@ -1076,27 +1076,36 @@ int64_t chunk_cap_tiles(int B, int max_len, int64_t total_len) {
   return sum < each ? sum : each;
 }
 
-// Which form a call takes, by what the two were measured to take (us; T:
-// tokens times KV heads).  Rebuilding: 30 and 0.84e-3 T at head_dim 128, half
-// at 64, however many rows follow.  By atoms: 45, the codes' way from HBM
-// (1.7e-4 T), the gathers and additions of every row pair (5.5e-5 T a pair),
-// and 20 for every pair that an SM starts on.  32 query and 8 KV heads, one
-// token: 2048 tokens 41 against 60, 8192 tokens 97 against 69, 32768 tokens 256
-// against 116; four tokens over 32768 254 against 185, eight 250 against 282.
-static bool by_atoms(int B, int64_t n_tok, int Hq, int Hkv, int d, int max_q, int max_len,
-                     int64_t total_len) {
+// Which form a call takes, by what the three were measured to take (us; T:
+// tokens times KV heads, half as much at head_dim 64).  Rebuilt for all:
+// 34 and 0.84e-3 T, however many rows follow.  In one pass: 9.5 and 1e-3 T, a
+// sixth more for 17 to 32 rows.  By atoms: a latency, the codes' way from HBM,
+// the gathers and additions of every row pair, and the segments of every pair
+// that an SM starts on.  32 query and 8 KV heads, us by tiles / in one pass /
+// by atoms: one token over 256: 15 / 12 / 77; over 2048: 36 / 26 / 47; over
+// 8192: 93 / 70 / 57; over 32768: 251 / 247 / 93; eight tokens over 2048: 36 /
+// 32 / 91, over 32768: 245 / 289 / 238.
+enum class Form { tiles, direct, atoms };
+static Form pick_form(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q, int max_len,
+                      int64_t total_len) {
   const int64_t q = max_q < n_tok ? max_q : n_tok, g = Hq / Hkv;
-  if (q < 1) return false;
+  if (q < 1) return Form::tiles;
   const double pairs = (double)((q * g + 1) / 2);
   const double all = min((double)B * pairs, (double)(n_tok * g + B) / 2) * Hkv;
   double T = (double)B * max_len;
   if (total_len > 0 && total_len < T) T = (double)total_len;
   T *= Hkv;
-  // an atom's sum over a share's tokens has to fit 32 bits with its roundings
-  // (half a unit, 16 words a token), and the pairs fit a grid
-  if (min((double)max_len, T * pairs / num_sms()) > (double)(1 << 24) || all > (double)(1 << 21))
-    return false;
-  return 45 + 1.7e-4 * T + 5.5e-5 * T * pairs + 20 * all / num_sms() < 30 + 0.84e-3 * T * (d / 128.0);
+  const double dt = d == 128 ? T : 0.55 * T, tiles = 34 + 0.84e-3 * dt;
+  const double direct = 9.5 + (q * g > 16 ? 1.17e-3 : 1e-3) * dt;
+  const double atoms = 30 + 7e-5 * T + 4e-5 * T * pairs + 9.0 * n / SDK_MAX_ATOMS +
+                       (15 + 22.0 * n / SDK_MAX_ATOMS) * all / num_sms();
+  const bool one_pass = direct_fits(B, n_tok, (int)g, max_q, max_len) && direct < tiles;
+  // by atoms, an atom's sum over a share's tokens has to fit 32 bits with its
+  // roundings (half a unit, 16 words a token), and the pairs fit a grid
+  if (min((double)max_len, T * pairs / num_sms()) <= (double)(1 << 24) && all <= (double)(1 << 21) &&
+      atoms < (one_pass ? direct : tiles))
+    return Form::atoms;
+  return one_pass ? Form::direct : Form::tiles;
 }
 
 // CTAs of the attention kernel: one per block, or one per SM with equal
@@ -1125,8 +1134,8 @@ static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
 
 size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len) {
-  if (!by_atoms(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len) &&
-      direct_fits(B, n_tok, Hq / Hkv, max_q, max_len))
+  const Form form = pick_form(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
+  if (form == Form::direct)
     return direct_workspace_bytes(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len);
   const int64_t q = max_q < n_tok ? max_q : n_tok;
   const int64_t blocks = cap_blocks(B, n_tok, Hq / Hkv, (int)q);
@@ -1134,7 +1143,7 @@ size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n
   const size_t a = chunk_layout(B, blocks, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.ctas,
                                 c.whole)
                        .total;
-  if (!by_atoms(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len)) return a;
+  if (form == Form::tiles) return a;
   const size_t b = atoms_workspace_bytes(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
   return a > b ? a : b;
 }
@@ -1185,12 +1194,13 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
                              cudaStream_t stream) {
   p.hdr = reinterpret_cast<WsHeader*>(workspace);
   p.plan = reinterpret_cast<ReqPlan*>(workspace + sizeof(WsHeader));
-  if (by_atoms(p.B, p.n_tok, p.Hq, p.Hkv, p.d, p.max_q, p.max_len, total_len)) {
+  const Form form =
+      pick_form(p.B, p.n_tok, p.Hq, p.Hkv, p.d, p.n, p.max_q, p.max_len, total_len);
+  if (form == Form::direct) return launch_chunk_direct(p, total_len, workspace, stream);
+  if (form == Form::atoms) {
     bool taken = false;
     const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
     if (taken) return s;
-  } else if (direct_fits(p.B, p.n_tok, p.g, p.max_q, p.max_len)) {
-    return launch_chunk_direct(p, total_len, workspace, stream);
   }
   const int64_t blocks = cap_blocks(p.B, p.n_tok, p.g, p.max_q);
   p.cap_work = blocks;

@@ -698,6 +698,26 @@ def test_serving_steps():
     assert len(set(live)) == len(live)
 
 
+@pytest.mark.parametrize("given", [(), ("slot_map",), ("cu_new", "n_free_out"), ("new_lens",)])
+def test_outputs_given_or_new(given):
+    """New outputs do not overlap each other, given ones are the ones returned."""
+    new = dict(slot_map=torch.full((7,), 99, device="cuda"), cu_new=_i32([9] * 4),
+               new_lens=_i32([9] * 3), n_free_out=_i32([9]))
+    r = sdk.sdk_block_tables(_i32([3, 0, 5]), _i32([2, 0, 3]), _i32([5, 4, 3, 2, 1, 0]), _i32([4]),
+                             _i32([[0, -1, -1], [-1] * 3, [4, 5, -1]]), 4, 7,
+                             **{k: new[k] for k in given})
+    got = dict(slot_map=r.slot_map, cu_new=r.cu_new, new_lens=r.new_lens, n_free_out=r.n_free)
+    assert all(got[k] is new[k] or got[k].data_ptr() == new[k].data_ptr() for k in given)
+    # request 0 takes page 2 (top of four), request 2 fills page 5: 5 + 3 = 8 tokens
+    assert r.block_table.tolist() == [[0, 2, -1], [-1] * 3, [4, 5, -1]]
+    assert r.slot_map.tolist() == [3, 8, 21, 22, 23, -1, -1]
+    assert r.cu_new.tolist() == [0, 2, 2, 5] and r.new_lens.tolist() == [5, 0, 8]
+    assert r.n_free.tolist() == [3]
+    for k, t in got.items():
+        t.zero_()
+        assert all(o is t or o.numel() == 0 or (o == 0).all() or k != n for n, o in got.items())
+
+
 def test_pages_released_twice_are_dropped():
     """What the stack has no place for is dropped; the stack stays where a
     captured plan reads it."""
