@@ -270,16 +270,20 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
     for (int t0 = t_begin; ; t0 += kStep) {
       const bool last = t0 + kStep >= t_end;
       // ---- keys and values of 32 tokens; those behind the share's are zero
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
+#pragma unroll 1
+      for (int i = 0; i < NU; ++i) {               // (unrolled, the code itself is slow to come)
         const int r = (i * kDirWarps + warp) * TPS + (rec >> 1);
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
         if (t0 + r - (rec >> 1) < t_end) {
           bool bad = false;
-          y = rebuild_piece<D, true>(p, dict, w[i], rec, sub, &bad);
+          y = rebuild_piece<D, true>(p, dict, w[0], rec, sub, &bad);
           if (bad) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
         }
         *reinterpret_cast<uint4*>((kv ? s_v[buf] : s_k) + r * kPitch + sub * 8) = y;
+#pragma unroll
+        for (int j = 1; j < NU; ++j)
+#pragma unroll
+          for (int k = 0; k < WPL; ++k) w[j - 1][k] = w[j][k];
       }
       if (!last) load_words(t0 + kStep);
       __syncthreads();

@@ -166,6 +166,21 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Two floats in a register pair, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Lane `sub` of the D / 8 that rebuild record `rec` of the warp: its eight
 // entries of sum_j c_j dict[i_j] as fp16.  w: the lane's 16 / (D / 8) code
 // words; ALL: all 16 atoms' rows in flight.  bad: an atom not in the
@@ -175,17 +190,14 @@ __device__ __forceinline__ uint4 rebuild_piece(const ChunkParams& p, const uint4
                                                const uint32_t (&w)[128 / D], int rec, int sub,
                                                bool* bad) {
   constexpr int LPR = D / 8, WPL = 16 / LPR;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
   auto word = [&](int j) { return __shfl_sync(0xffffffffu, w[j % WPL], rec * LPR + j / WPL); };
   auto add = [&](float c, const uint4& v) {
-    acc[0] = fmaf(c, bf16_lo(v.x), acc[0]);
-    acc[1] = fmaf(c, bf16_hi(v.x), acc[1]);
-    acc[2] = fmaf(c, bf16_lo(v.y), acc[2]);
-    acc[3] = fmaf(c, bf16_hi(v.y), acc[3]);
-    acc[4] = fmaf(c, bf16_lo(v.z), acc[4]);
-    acc[5] = fmaf(c, bf16_hi(v.z), acc[5]);
-    acc[6] = fmaf(c, bf16_lo(v.w), acc[6]);
-    acc[7] = fmaf(c, bf16_hi(v.w), acc[7]);
+    const uint64_t cc = pack2(c, c);
+    acc[0] = fma2(cc, pack2(bf16_lo(v.x), bf16_hi(v.x)), acc[0]);
+    acc[1] = fma2(cc, pack2(bf16_lo(v.y), bf16_hi(v.y)), acc[1]);
+    acc[2] = fma2(cc, pack2(bf16_lo(v.z), bf16_hi(v.z)), acc[2]);
+    acc[3] = fma2(cc, pack2(bf16_lo(v.w), bf16_hi(v.w)), acc[3]);
   };
   auto atom = [&](uint32_t x) {
     const uint32_t a = word_idx(x);
@@ -212,7 +224,8 @@ __device__ __forceinline__ uint4 rebuild_piece(const ChunkParams& p, const uint4
   __half2 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float x0 = acc[2 * i], x1 = acc[2 * i + 1];
+    float x0, x1;
+    unpack2(acc[i], &x0, &x1);
     if (!(fabsf(x0) <= 65504.0f)) {
       *bad = true;
       x0 = x0 != x0 ? 0.0f : copysignf(65504.0f, x0);
