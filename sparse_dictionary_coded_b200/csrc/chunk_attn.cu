@@ -122,6 +122,58 @@ __device__ void plan_blocks(const ChunkParams& p, const int32_t* s_block, int64_
   }
 }
 
+// One CTA, p.parts (at most a block of rows per thread, blocks * Hkv <= ctas):
+// cuts every block's tiles into parts of S, S the smallest that leaves no more
+// parts than CTAs and not too many to join; p.units: the parts before every block, per KV head.
+__device__ void plan_parts(const ChunkParams& p, const int32_t* s_block, int64_t* s_warp) {
+  __shared__ int s_tiles[kRebThreads];   // -1: a refused request's
+  const int blocks = s_block[p.B], m = threadIdx.x, lane = threadIdx.x & 31;
+  __syncthreads();                     // the plan is written
+  int tiles = -1;
+  if (m < blocks) {
+    const int b = find_first(s_block, p.B, m);
+    int at;
+    const ReqPlan r = p.plan[b];
+    if (r.n > 0) block_tiles(p, r, m - s_block[b], &at, &tiles);
+  }
+  s_tiles[m] = tiles;
+  __syncthreads();
+  const int room = p.ctas / p.Hkv;
+  int S = 1;
+  auto parts_of = [&](int t) { return t < 0 ? 0 : max((t + S - 1) / S, 1); };
+  auto sum_of = [&](auto f) {
+    int v = 0;
+    for (int i = lane; i < blocks; i += 32) v += f(s_tiles[i]);
+    return __reduce_add_sync(0xffffffffu, v);
+  };
+  S = max((sum_of([](int t) { return max(t, 0); }) + room - 1) / room, 1);
+  // a tile takes 1.6 us, a part of a row 0.35 us when joining: 4.5 S^2 >= tiles
+  int most = 0;
+  for (int i = lane; i < blocks; i += 32) most = max(most, s_tiles[i]);
+  most = __reduce_max_sync(0xffffffffu, most);
+  while (9 * (int64_t)S * S < 2 * most) ++S;
+  while (sum_of(parts_of) > room) S += (S + 7) / 8;   // (one part a block fits)
+  int64_t total;
+  const int64_t upto = block_scan64(parts_of(tiles), s_warp, &total);
+  if (m < blocks) p.units[m + 1] = upto;
+  if (m == 0) p.units[0] = 0;
+  for (int b = threadIdx.x; b <= p.B; b += kRebThreads) {
+    p.plan[b].pair0 = s_block[b];
+    if (b == p.B) {
+      p.plan[b].npair = (int)total * p.Hkv;
+      p.plan[b].ntiles = S;
+    }
+  }
+}
+
+__device__ __forceinline__ void plan_work(const ChunkParams& p, const int32_t* s_block,
+                                          int64_t* s_warp) {
+  if (p.parts)
+    plan_parts(p, s_block, s_warp);
+  else
+    plan_blocks(p, s_block, s_warp);
+}
+
 constexpr int kPackSteps = 4;
 
 // The query rows as tiles of packed rows (row = token * g + head of the
@@ -190,7 +242,7 @@ __global__ void __launch_bounds__(kRebThreads) chunk_prep_kernel(ChunkParams p) 
   pdl_launch();
   make_plan<false>(p, blockIdx.x == 0, s_tile0, s_block, s_warp);
   pack_queries<D>(p, s_block, blockIdx.x, gridDim.x);
-  if (blockIdx.x == 0) plan_blocks(p, s_block, s_warp);
+  if (blockIdx.x == 0) plan_work(p, s_block, s_warp);
 }
 
 // The rebuilt tiles.  Every CTA scans the requests' tile counts itself.  D / 8
@@ -214,7 +266,7 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
   int start = (int)blockIdx.x, stride = (int)gridDim.x;
   if (TOK == 1) {
     if (blockIdx.x == 0 && gridDim.x > 1) {
-      plan_blocks(p, s_block, s_warp);
+      plan_work(p, s_block, s_warp);
       return;
     }
     if (gridDim.x > 1) {
@@ -223,7 +275,7 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
     }
     // from the last CTA on: the first ones have most of the items
     pack_queries<D>(p, s_block, stride - 1 - start, stride);
-    if (gridDim.x == 1) plan_blocks(p, s_block, s_warp);
+    if (gridDim.x == 1) plan_work(p, s_block, s_warp);
   }
 
   constexpr int LPR = D / 8;           // lanes per record
@@ -296,9 +348,9 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
 // rescaled in TMEM, which is rare); P is 2^7 above its nominal range, so it
 // stays below 2^15 and its smallest fp16 step is 2^-31 of the row's largest
 // term: what 2^18 tokens lose by it is below 2^-13.
-// A CTA takes a block (256 packed rows of a KV head), or an equal share of all
-// blocks' tiles (chunk_cut says which); a block that a share's end cuts leaves
-// partial sums that chunk_join_kernel joins.
+// A CTA takes a block (256 packed rows of a KV head), a part of one, or an
+// equal share of all blocks' tiles (chunk_cut says which); a block in several
+// parts or shares leaves partial sums that chunk_join_kernel joins.
 // 2048 tokens over 32768, 32 heads: 910 us of 1248, 1170 TFLOP/s; the tensor
 // pipe is busy two thirds of a tile's 3000 cycles, the rest is the chain score
 // - maximum - exponentials - P of a row (1800 cycles) that the other tile's
@@ -522,6 +574,13 @@ struct Walk {
     end = units();
     return true;
   }
+  // of that block only part k of S tiles
+  __device__ __forceinline__ void part(int k, int S) {
+    if (count == 0) return;
+    const int t0 = k * S, t1 = min(t0 + S, count);
+    off = k > 0 ? kBlockCost + t0 : 0;
+    end = kBlockCost + t1 - off;
+  }
   __device__ __forceinline__ int units() const { return block_units(count); }   // of the block
   // units of the segment that starts at u
   __device__ __forceinline__ int take() const {
@@ -557,7 +616,7 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
   const int g = p.g;
   pdl_launch();
   pdl_wait();
-  int64_t u0 = 0, u1 = 0;
+  int64_t u0 = 0, cut_lo = 0, cut_hi = 0;          // what chunk_join_kernel is told
   Walk walk;
   if (p.whole) {                                   // CTA = block
     // a head's blocks side by side, so that their CTAs read the same tiles at
@@ -566,13 +625,25 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
     if (blocks == 0) return;
     const int head = (int)blockIdx.x / blocks, m = blocks - 1 - (int)blockIdx.x % blocks;
     if (head >= p.Hkv || !walk.whole(p, m, head)) return;
+  } else if (p.parts) {                            // CTA = part of a block
+    const int blocks = p.plan[p.B].pair0, S = p.plan[p.B].ntiles, item = (int)blockIdx.x;
+    if (item >= p.plan[p.B].npair) return;
+    const int m = warp_search(blocks, item, [&](int i) { return p.units[i] * p.Hkv; });
+    const int first = (int)p.units[m] * p.Hkv, n = (int)(p.units[m + 1] - p.units[m]);
+    const int head = (item - first) / n, k = (item - first) - head * n;
+    if (!walk.whole(p, m, head)) return;
+    walk.part(k, S);
+    u0 = item;                                     // its parts count as units
+    cut_lo = item - k;
+    cut_hi = cut_lo + n;
   } else {
     const int64_t total = p.plan[p.B].work0;
     const int shares = p.plan[p.B].npair;
     if ((int)blockIdx.x >= shares) return;
     u0 = total * blockIdx.x / shares;
-    u1 = total * (blockIdx.x + 1) / shares;
-    walk.start(p, u0, u1);
+    walk.start(p, u0, total * (blockIdx.x + 1) / shares);
+    cut_lo = u0 - walk.off;
+    cut_hi = cut_lo + walk.units();
   }
   uint8_t* smem = tc::align_smem_1k(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -779,8 +850,8 @@ __global__ void __launch_bounds__(kAThreads, 1) chunk_attn_kernel(ChunkParams p)
     if (tid == 0 && !p.whole) {
       Cut cut;
       cut.u0 = u0;
-      cut.lo = u0 - w.off;
-      cut.hi = cut.lo + w.units();
+      cut.lo = cut_lo;
+      cut.hi = cut_hi;
       cut.row0 = w.rp.row0;
       cut.rows = w.rp.n * g;
       cut.mb = w.mb;
@@ -1094,25 +1165,29 @@ static Form pick_form(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int m
   return one_pass ? Form::direct : Form::tiles;
 }
 
-// CTAs of the attention kernel: one per block, or one per SM with equal
-// shares.  A CTA per block where all contexts are short and the blocks fit the
-// SMs (eight chats of up to 600 tokens: 20 us, with shares 32 us), and where
-// the blocks fill whole rounds of the SMs (their CTAs read a tile together;
-// 2048 tokens over 32768, 256 blocks: 1250 us, with shares 1300 us).  Shares
-// where there are too few blocks (twelve mixed requests: 33 us, with a CTA per
-// block 37 us).
+// CTAs of the attention kernel.  Where the blocks fit the SMs, one for every
+// part of a block, the parts of equal length (twelve mixed requests: 27.6 us, in
+// equal shares 30.6 us: a share that ends one block and begins another fills
+// and drains its pipeline twice), but whole blocks where no context is longer
+// than 8 tiles and an eighth of the SMs have one (a prompt of 512 tokens, 64
+// blocks: 26 us, in parts 31 us; 256 tokens over 444, 4 blocks: 24 us, in parts
+// 20 us).  A CTA per block too where the blocks fill whole rounds of the SMs
+// (their CTAs read a tile together; 2048 tokens over 32768, 256 blocks: 1250
+// us, with shares 1300 us), else one per SM with equal shares.
 struct ChunkCut {
   int ctas;
-  bool whole;
+  bool whole, parts;
 };
 static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
   const int64_t tiles = (max_len + (int64_t)kTile - 1) / kTile, items = blocks * Hkv, sms = num_sms();
   const int64_t rounds = (items + sms - 1) / sms;
-  ChunkCut c;
-  c.whole = rounds <= 1 ? tiles <= 8 : 5 * items >= 4 * rounds * sms;
-  if (items > 0x7FFFFFFF) c.whole = false;
   int64_t most = min(sms, (int64_t)kMaxShares);
+  ChunkCut c;
+  c.parts = items <= most && blocks <= kRebThreads && (tiles > 8 || 8 * items <= sms);
+  c.whole = !c.parts && (rounds <= 1 ? tiles <= 8 : 5 * items >= 4 * rounds * sms);
+  if (items > 0x7FFFFFFF) c.whole = false;
   if (c.whole) most = items;
+  else if (c.parts) most = min(most, items * tiles);
   else if (items * (tiles + kBlockCost) < 4 * most) most = (items * (tiles + kBlockCost) + 3) / 4;
   c.ctas = (int)(most < 1 ? 1 : most);
   return c;
@@ -1193,6 +1268,7 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
   const ChunkCut c = chunk_cut(blocks, p.Hkv, p.max_len);
   p.ctas = c.ctas;
   p.whole = c.whole ? 1 : 0;
+  p.parts = c.parts ? 1 : 0;
   const ChunkLayout l = chunk_layout(p.B, blocks, p.Hkv, p.d, p.cap_tiles, c.ctas, c.whole);
   p.cuts = workspace + l.cuts;
   p.units = reinterpret_cast<int64_t*>(workspace + l.units);

@@ -55,7 +55,7 @@ struct ChunkParams {
   float* lse;
   WsHeader* hdr;
   ReqPlan* plan;         // [B + 1], the last one the totals
-  // by tiles: running sums of the blocks' tiles, rebuilt key and value tiles
+  // by tiles: running sums of the blocks' tiles (or parts), rebuilt key and value tiles
   // [tile][Hkv][tile image], partial sums [2 x CTA][256 rows][..]
   int64_t* units;
   char* cuts;            // what every share starts with
@@ -75,7 +75,7 @@ struct ChunkParams {
   int64_t n_tok, cap_pairs, cap_work;
   int B, Hq, Hkv, g, d, n, n_pad, n_pages, page_size, max_pages;
   int max_q, max_len, window, causal, cap_tiles;
-  int ctas, whole, ksplits, row_tiles;
+  int ctas, whole, parts, ksplits, row_tiles;
   float scale;
 };
 

@@ -341,6 +341,10 @@ SHAPES = [
     dict(lens=[70000, 3], new=[1, 1], Hq=1, Hkv=1, n=32767, P=7),     # one row of a pair
     dict(lens=[1100] * 30, new=[1] * 30, Hq=4, Hkv=2, n=513, d=64),   # many requests
     dict(lens=[150000], new=[1], Hq=3, Hkv=1, n=2, P=64),             # two atoms
+    dict(lens=[9000, 5, 1300], new=[40, 5, 100], Hq=4, Hkv=1, n=300, d=64, P=24),  # blocks in parts
+    dict(lens=[1500] * 40, new=[30] * 40, Hq=8, Hkv=4, n=300, d=64, P=16),   # equal shares of them
+    dict(lens=[700, 0, 90, 30] * 20, new=[3, 0, 2, 1] * 20, Hq=6, Hkv=3, n=400, P=8),  # many requests in one pass
+    dict(lens=[2000, 17, 16, 33], new=[8, 8, 1, 4], Hq=4, Hkv=1, n=300, P=16),   # 32 rows in one pass
     dict(lens=[33000, 100], new=[40, 2], Hq=4, Hkv=1, P=32),          # one block shared by all SMs
     dict(lens=[2500], new=[2500], Hq=32, Hkv=8, n=300, d=64, P=64),   # more blocks than SMs
 ]
