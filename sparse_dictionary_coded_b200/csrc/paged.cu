@@ -43,11 +43,12 @@ __device__ __forceinline__ uint32_t block_sat_scan(uint32_t v, uint32_t* s_warp,
 // One step's plan.  Every CTA scans the requests itself (rows, then pages:
 // two scans of at most 4096 values in shared memory cost a few hundred ns, a
 // second launch or a grid-wide wait would cost more), then takes its share
-// of the table entries and of the slots by binary search in the scans, four
-// rows a thread at a time.  The page of a slot comes from the free stack when
+// of the table entries and of the slots by binary search in the scans; of many
+// rows a thread takes four neighbours.  The page of a slot comes from the free stack when
 // this call assigns it, so no CTA reads an entry another one writes.  Bound
 // by its launch and the chain load - scan - load for a step of single tokens
-// (3.7 us for 4 requests), by the 8-byte writes of slot_map for prompts.
+// (2.7 us for 4 requests in a graph), for prompts too (64 of up to 16384 tokens:
+// 4.7 us; four rows far apart, a search each: 6.4 us).
 // T threads: 256 for up to 256 requests, else 1024.
 template <int T>
 __global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
@@ -59,6 +60,11 @@ __global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
   const int tid = threadIdx.x;
   const uint32_t P = (uint32_t)p.page_size;
   int n_free = *p.n_free;
+  int len0 = 0, n0 = 0;                 // the first requests', loaded beside it
+  if (tid < p.B) {
+    len0 = p.lens[tid];
+    n0 = p.n_new[tid];
+  }
   if (n_free < 0 || n_free > p.n_stack) {
     if (tid == 0 && blockIdx.x == 0) record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x70000001u);
     n_free = min(max(n_free, 0), p.n_stack);
@@ -67,11 +73,12 @@ __global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
   uint32_t row0 = 0, page0 = 0;
   for (int b0 = 0; b0 < p.B; b0 += T) {
     const int b = b0 + tid;
-    int len = 0, n = 0;
-    if (b < p.B) {
+    int len = len0, n = n0;
+    if (b0 > 0 && b < p.B) {
       len = p.lens[b];
       n = p.n_new[b];
     }
+    if (b >= p.B) len = n = 0;
     uint32_t rows, pages;
     const uint32_t row1 = sat_add(row0, block_sat_scan<T>((uint32_t)max(n, 0), s_warp, &rows));
     // refused: 1 a bound or the pool, 2 a bad length
@@ -106,22 +113,23 @@ __global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
     page0 = sat_add(page0, pages);
   }
   __syncthreads();
-  // s_fresh of a request behind the one that did not fit: the pages taken
-  // before it are those of the last request that fitted
-  __shared__ int s_taken;
-  if (tid == 0) s_taken = 0;
-  __syncthreads();
-  {
+  int taken = (int)page0;
+  if (page0 > (uint32_t)n_free) {
+    // s_fresh of a request behind the one that did not fit: the pages taken
+    // before it are those of the last request that fitted
+    __shared__ int s_taken;
+    if (tid == 0) s_taken = 0;
+    __syncthreads();
     int m = 0;
     for (int b = tid; b < p.B; b += T) m = max(m, s_fresh[b + 1]);
     m = (int)__reduce_max_sync(0xffffffffu, m);
     if ((tid & 31) == 0 && m > 0) atomicMax(&s_taken, m);
+    __syncthreads();
+    taken = s_taken;
+    for (int b = tid; b < p.B; b += T)
+      if (s_fresh[b + 1] < 0) s_fresh[b + 1] = taken;
+    __syncthreads();
   }
-  __syncthreads();
-  const int taken = s_taken;
-  for (int b = tid; b < p.B; b += T)
-    if (s_fresh[b + 1] < 0) s_fresh[b + 1] = taken;
-  __syncthreads();
   if (blockIdx.x == 0) {
     for (int b = tid; b <= p.B; b += T) p.cu_new[b] = s_row[b];
     if (tid == 0) *p.n_free_out = n_free - taken;
@@ -149,65 +157,107 @@ __global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
     p.table[(int64_t)b * p.max_pages + have + ((int)e - s_fresh[b])] = fresh_page((int)e);
   }
   const int n_rows = s_row[p.B];
+  // the page that holds token pos of request b, column col
+  auto page_at = [&](int b, int len, uint32_t col, bool* fresh) {
+    const uint32_t have = ((uint32_t)len + P - 1) / P;
+    *fresh = col >= have;
+    return *(*fresh ? p.free_pages + (n_free - 1 - (s_fresh[b] + (int)(col - have)))
+                    : p.table + ((int64_t)b * p.max_pages + col));
+  };
+  auto slot_of = [&](int b, int pg, uint32_t off, bool fresh) {
+    if (pg >= 0 && pg < p.n_pages) return (int64_t)pg * P + off;
+    if (!fresh)                         // (a bad page of the stack is recorded above)
+      record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x73000000u | (uint32_t)b);
+    return (int64_t)-1;
+  };
   constexpr int R = 4;                  // rows a thread has in flight
-  for (int64_t r0 = t0; r0 < p.max_new; r0 += R * step) {
-    int64_t slot[R];
+  if (p.max_new <= 2 * step) {
+    for (int64_t r0 = t0; r0 < p.max_new; r0 += step) {
+      int64_t slot = -1;
+      if (r0 < n_rows) {
+        const int b = find(s_row, (int)r0), len = s_len[b];
+        if (len >= 0) {
+          const uint32_t pos = (uint32_t)len + (uint32_t)((int)r0 - s_row[b]), col = pos / P;
+          bool fresh;
+          const int pg = page_at(b, len, col, &fresh);
+          slot = slot_of(b, pg, pos - col * P, fresh);
+        }
+      }
+      p.slot_map[r0] = slot;
+    }
+    return;
+  }
+  // many rows: four neighbours a thread, so that one search does for most
+  const bool wide = ((uintptr_t)p.slot_map & 15) == 0;
+  for (int64_t r0 = t0 * R; r0 < p.max_new; r0 += R * step) {
+    int req[R], pg[R];
+    uint32_t off[R];
+    bool fresh[R];
+    int b = r0 < n_rows ? find(s_row, (int)r0) : 0, len = s_len[b];
+    uint32_t pos = (uint32_t)len + (uint32_t)((int)min(r0, (int64_t)n_rows) - s_row[b]), col = pos / P,
+             o = pos - col * P;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const int64_t r = r0 + k * step;
-      slot[k] = -1;
-      if (r >= n_rows) continue;
-      const int b = find(s_row, (int)r);
-      const int len = s_len[b];
-      if (len < 0) continue;
-      const uint32_t pos = (uint32_t)len + (uint32_t)((int)r - s_row[b]);
-      const uint32_t col = pos / P, have = ((uint32_t)len + P - 1) / P;
-      const bool fresh = col >= have;
-      const int pg = *(fresh ? p.free_pages + (n_free - 1 - (s_fresh[b] + (int)(col - have)))
-                             : p.table + ((int64_t)b * p.max_pages + col));
-      if (pg >= 0 && pg < p.n_pages)
-        slot[k] = (int64_t)pg * P + (pos - col * P);
-      else if (!fresh)                  // (a bad page of the stack is recorded above)
-        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x73000000u | (uint32_t)b);
+      const int64_t r = r0 + k;
+      req[k] = -1;
+      if (r < n_rows) {
+        if (r >= s_row[b + 1]) {        // the next request with rows
+          do ++b;
+          while (r >= s_row[b + 1]);
+          len = s_len[b];
+          col = (uint32_t)len / P;
+          o = (uint32_t)len - col * P;
+        }
+        if (len >= 0) {
+          req[k] = b;
+          off[k] = o;
+          pg[k] = page_at(b, len, col, &fresh[k]);
+        }
+        if (++o == P) {
+          o = 0;
+          ++col;
+        }
+      }
     }
+    int64_t slot[R];
 #pragma unroll
     for (int k = 0; k < R; ++k)
-      if (r0 + k * step < p.max_new) p.slot_map[r0 + k * step] = slot[k];
+      slot[k] = req[k] < 0 ? -1 : slot_of(req[k], pg[k], off[k], fresh[k]);
+    if (wide && r0 + R <= p.max_new) {
+      longlong2* dst = reinterpret_cast<longlong2*>(p.slot_map + r0);
+      dst[0] = make_longlong2(slot[0], slot[1]);
+      dst[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (r0 + k < p.max_new) p.slot_map[r0 + k] = slot[k];
+    }
   }
 }
 
 // Eight lanes copy one (token, KV head): four 16-byte pieces of key words,
-// four of value words, to the 128-byte line of its slot; a thread has four
-// pieces in flight.  Bound by HBM (the words are read once and written once).
-// I: the type that counts the pieces.
+// four of value words, to the 128-byte line of its slot.  Bound by HBM (the
+// words are read once and written once): 16384 tokens of 8 heads, 33.7 MB, 8.2
+// us, 5.3 in a graph.  One piece a thread: of four, all read before the first
+// was written (10.2 us), of eight 15.8 us.  I: the type that counts the pieces.
 template <typename I>
 __global__ void __launch_bounds__(256) paged_store_kernel(StoreParams p) {
-  constexpr int R = 4;
   const I items = (I)p.n_tok * (I)(p.Hkv * 8), step = (I)gridDim.x * 256;
-  for (I e0 = (I)blockIdx.x * 256 + threadIdx.x; e0 < items; e0 += R * step) {
-    uint4 v[R];
-    int64_t at[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const I e = e0 + k * step;
-      at[k] = -1;
-      if (e >= items) continue;
-      const I rec = e >> 3, t = rec / (I)p.Hkv;
-      const int c = (int)(e & 7), h = (int)(rec - t * (I)p.Hkv);
-      v[k] = __ldg(reinterpret_cast<const uint4*>(c < 4 ? p.codes_k : p.codes_v) + rec * 4 + (c & 3));
-      const int64_t slot = __ldg(p.slot_map + t);
-      if (slot < 0) continue;
-      if (slot >= (int64_t)p.n_pages * p.page_size) {
-        record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x74000000u);
-        continue;
-      }
+  for (I e = (I)blockIdx.x * 256 + threadIdx.x; e < items; e += step) {
+    const I rec = e >> 3, t = rec / (I)p.Hkv;
+    const int c = (int)(e & 7), h = (int)(rec - t * (I)p.Hkv);
+    const uint4 v =
+        __ldg(reinterpret_cast<const uint4*>(c < 4 ? p.codes_k : p.codes_v) + rec * 4 + (c & 3));
+    const int64_t slot = __ldg(p.slot_map + t);
+    int64_t at = -1;                    // (one store at the end: both loads are issued first)
+    if (slot >= (int64_t)p.n_pages * p.page_size) {
+      record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x74000000u);
+    } else if (slot >= 0) {
       const uint32_t page = (uint32_t)slot / (uint32_t)p.page_size;
       const uint32_t off = (uint32_t)slot - page * (uint32_t)p.page_size;
-      at[k] = (((int64_t)page * p.Hkv + h) * p.page_size + off) * 8 + c;
+      at = (((int64_t)page * p.Hkv + h) * p.page_size + off) * 8 + c;
     }
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (at[k] >= 0) reinterpret_cast<uint4*>(p.pages)[at[k]] = v[k];
+    if (at >= 0) reinterpret_cast<uint4*>(p.pages)[at] = v;
   }
 }
 
@@ -235,9 +285,9 @@ sdk_status launch_block_tables(const TableParams& p, cudaStream_t stream) {
 sdk_status launch_paged_store(const StoreParams& p, cudaStream_t stream) {
   if (p.n_tok == 0) return SDK_OK;
   const int64_t items = p.n_tok * p.Hkv * 8;
-  int64_t grid = (items + 1023) / 1024;
-  if (grid > 32 * num_sms()) grid = 32 * num_sms();
-  // e0 + 3 steps stays below 2^32 for the small type
+  int64_t grid = (items + 255) / 256;
+  if (grid > 128 * num_sms()) grid = 128 * num_sms();
+  // an index and a step stay below 2^32 for the small type
   if (items <= (int64_t)1 << 31)
     paged_store_kernel<uint32_t><<<(unsigned)grid, 256, 0, stream>>>(p);
   else

@@ -702,6 +702,56 @@ def test_serving_steps():
     assert len(set(live)) == len(live)
 
 
+@pytest.mark.parametrize("P", [1, 3, 64])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_many_rows(P, shift):
+    """Slots of thousands of rows: idle requests, requests of one and of many
+    rows, refused ones, a map at an odd address and of an odd length."""
+    g = torch.Generator().manual_seed(P)
+    lens = torch.randint(0, 50, (300,), generator=g).tolist()
+    new = [0 if i % 5 == 0 else 1 if i % 5 == 1 else int(torch.randint(1, 90, (1,), generator=g))
+           for i in range(300)]
+    lens[7], new[299] = -1, 1 << 30                      # refused
+    cols = 200
+    have = [max(-(-x // P), 0) for x in lens]
+    pool = sum(-(-(x + n) // P) for x, n in zip(lens, new) if 0 <= x and n < 1 << 20)
+    table = torch.full((300, cols), -1, dtype=torch.int32)
+    at = 0
+    for b, k in enumerate(have):
+        table[b, :k] = torch.arange(at, at + k)
+        at += k
+    free = list(range(at, pool))[::-1]
+    max_new = sum(n for n in new if n < 1 << 20) + 1001
+    # what is wanted, request by request (the last one passes max_new)
+    want, pos, over, k, asked = [], 0, False, 0, 0
+    for b in range(300):
+        pos += max(new[b], 0)
+        over = pos > max_new
+        if lens[b] < 0 or over:
+            want += [-1] * (0 if over else new[b])
+            continue
+        # (request 299's own pages are not among those of the pool that the
+        # step asks for: the last pages are missing, and a request that needs
+        # one is refused)
+        need = -(-(lens[b] + new[b]) // P) - have[b]
+        asked += need
+        if need > 0 and asked > len(free):
+            want += [-1] * new[b]
+            continue
+        pages = table[b, :have[b]].tolist()
+        while len(pages) * P < lens[b] + new[b]:
+            pages.append(free[len(free) - 1 - k])
+            k += 1
+        want += [pages[t // P] * P + t % P for t in range(lens[b], lens[b] + new[b])]
+    want += [-1] * (max_new - len(want))
+    room = torch.full((max_new + 2,), 77, dtype=torch.int64, device="cuda")
+    out = room[shift:shift + max_new]
+    r = sdk.sdk_block_tables(_i32(lens), _i32(new), _i32(free), _i32([len(free)]), table.cuda(), P,
+                             max_new, n_pages=pool, slot_map=out)
+    assert r.slot_map.tolist() == want and r.n_free.tolist() == [len(free) - k]
+    assert room[:shift].tolist() == [77] * shift and room[shift + max_new:].tolist() == [77] * (2 - shift)
+
+
 @pytest.mark.parametrize("given", [(), ("slot_map",), ("cu_new", "n_free_out"), ("new_lens",)])
 def test_outputs_given_or_new(given):
     """New outputs do not overlap each other, given ones are the ones returned."""
