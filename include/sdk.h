@@ -517,7 +517,7 @@ SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dt
  *   over long contexts go by atoms (scores from <q, D_K>, values through
  *   weights per atom).  Results of one form do not depend on the other
  *   requests' contents, but their last bits may on how the batch cuts the
- *   contexts.
+ *   contexts.  The host's bounds choose the form: tight ones choose better.
  * Arithmetic: rebuilt vectors and probabilities (by atoms: <q, D_K>) enter
  *   the products in fp16 (fp32 sums), weights per atom with 16 significand
  *   bits; q exactly.  A rebuilt entry beyond +-65504 or NaN is recorded

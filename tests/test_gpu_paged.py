@@ -301,17 +301,18 @@ class Case:
             total_len=sum(self.lens) if total is None else total, causal=causal, window=window,
             workspace=ws, **kw)
 
-    def workspace(self):
+    def workspace(self, max_q=None, max_len=None, total=None):
         T, Hq, d = self.q.shape
         return sdk.new_workspace(sdk.sdk_chunk_attn_workspace_bytes(
-            len(self.lens), T, Hq, self.pages.shape[1], d, self.dk.shape[0], max(max(self.new), 1),
-            max(max(self.lens), 1), sum(self.lens)))
+            len(self.lens), T, Hq, self.pages.shape[1], d, self.dk.shape[0],
+            max_q or max(max(self.new), 1), max_len or max(max(self.lens), 1),
+            sum(self.lens) if total is None else total))
 
-    def check(self, causal=True, window=0, scale=None):
+    def check(self, causal=True, window=0, scale=None, **bounds):
         T, Hq, d = self.q.shape
-        ws = self.workspace()
+        ws = self.workspace(**bounds)
         lse = torch.full((T, Hq), 77.0, device="cuda")
-        out = self.run(causal, window, ws, lse=lse, scale=scale)
+        out = self.run(causal, window, ws, lse=lse, scale=scale, **bounds)
         assert _status(ws) == (0, 0)
         want, tol, wl, el = _attend_ref(self.q, self.dk, self.dv, self.pages, self.table, self.lens,
                                         self.cu, causal, window, scale or 1 / math.sqrt(d))
@@ -575,6 +576,16 @@ def test_offsets_that_fall_stay_inside():
     c.cu = [0] + [400 - 10 * (i % 40) for i in range(40)]
     c.run(ws=ws[:n])
     assert _status(ws)[0] in (3, 6) and (ws[n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("bounds", [dict(max_len=600), dict(max_len=4096, total=0),
+                                    dict(max_len=65536, total=0), dict(max_q=64, max_len=600, total=0),
+                                    dict(max_q=64, max_len=65536, total=0)], ids=str)
+@pytest.mark.parametrize("new", [[1, 1, 0, 1], [3, 17, 0, 2], [60, 17, 0, 2]])
+@pytest.mark.parametrize("window", [0, 50])
+def test_loose_bounds(new, bounds, window):
+    """Bounds far above the lengths choose another form, not another result."""
+    Case([300, 17, 0, 600], new, n=2000, cols=4096, seed=18).check(window=window, **bounds)
 
 
 def test_many_requests():
