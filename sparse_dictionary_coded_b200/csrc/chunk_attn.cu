@@ -1171,7 +1171,8 @@ static Form pick_form(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int m
 // and drains its pipeline twice), but whole blocks where no context is longer
 // than 8 tiles and an eighth of the SMs have one (a prompt of 512 tokens, 64
 // blocks: 26 us, in parts 31 us; 256 tokens over 444, 4 blocks: 24 us, in parts
-// 20 us).  A CTA per block too where the blocks fill whole rounds of the SMs
+// 20 us), or than 3 tiles (20 tokens of 200: 17.4 us, in parts 18.8 us; of 700:
+// 26 and 24 us).  A CTA per block too where the blocks fill whole rounds of the SMs
 // (their CTAs read a tile together; 2048 tokens over 32768, 256 blocks: 1250
 // us, with shares 1300 us), else one per SM with equal shares.
 struct ChunkCut {
@@ -1183,7 +1184,7 @@ static ChunkCut chunk_cut(int64_t blocks, int Hkv, int max_len) {
   const int64_t rounds = (items + sms - 1) / sms;
   int64_t most = min(sms, (int64_t)kMaxShares);
   ChunkCut c;
-  c.parts = items <= most && blocks <= kRebThreads && (tiles > 8 || 8 * items <= sms);
+  c.parts = items <= most && blocks <= kRebThreads && (tiles > 8 || (tiles > 3 && 8 * items <= sms));
   c.whole = !c.parts && (rounds <= 1 ? tiles <= 8 : 5 * items >= 4 * rounds * sms);
   if (items > 0x7FFFFFFF) c.whole = false;
   if (c.whole) most = items;
