@@ -26,6 +26,15 @@ constexpr int kTokThreads = 640;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Shares that `work` units are cut into, none of them empty: of a thousand
+// tokens at least (fewer would leave threads idle), `most` of them at most.
+// The host sizes the launch by the bound on the work, the device cuts the work
+// there is: a share without a unit would leave its sums unwritten.
+__host__ __device__ __forceinline__ int share_count(int64_t work, int most) {
+  const int64_t want = work / 1024;
+  return (int)(want < 1 ? 1 : want > most ? most : want);
+}
+
 struct AtomCut {
   int64_t pairs, work;             // bounds
   int ctas, row_tiles, ksplits, chunks, n_pad;
@@ -42,10 +51,7 @@ AtomCut atom_cut(int B, int64_t n_tok, int Hq, int Hkv, int n, int max_q, int ma
   int64_t tokens = (int64_t)B * max_len;
   if (total_len > 0 && total_len < tokens) tokens = total_len;
   c.work = tokens * Hkv * each;
-  // a share below a thousand tokens would leave threads idle
-  const int64_t want = c.work / 1024;
-  const int most = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
-  c.ctas = (int)(want < 1 ? 1 : want > most ? most : want);
+  c.ctas = share_count(c.work, num_sms() < kMaxCtas ? num_sms() : kMaxCtas);
   // a segment is a CTA's share of one pair: at most ctas + pairs of them
   c.row_tiles = (int)((2 * (c.ctas + c.pairs) + kN - 1) / kN);
   c.chunks = (n + kChunk - 1) / kChunk;
@@ -519,9 +525,10 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   pdl_launch();
   pdl_wait();
   const int64_t W = p.plan[p.B].work0;
-  int64_t w = W * blockIdx.x / gridDim.x;
-  const int64_t w_end = W * (blockIdx.x + 1) / gridDim.x;
-  if (w >= w_end) return;
+  const int shares = share_count(W, p.ctas);
+  if (W == 0 || (int)blockIdx.x >= shares) return;
+  int64_t w = W * blockIdx.x / shares;
+  const int64_t w_end = W * (blockIdx.x + 1) / shares;
   int b;
   {
     int lo = 0, hi = p.B;
@@ -836,7 +843,7 @@ __global__ void __launch_bounds__(128, 1)
   pdl_launch();
   pdl_wait();
   // rows that no segment wrote are not read
-  const int rows = 2 * (p.ctas + p.plan[p.B].pair0);
+  const int rows = 2 * (share_count(p.plan[p.B].work0, p.ctas) + p.plan[p.B].pair0);
   if ((int)blockIdx.y * kN >= rows) return;
   const int chunks = (p.n + kChunk - 1) / kChunk;
   const int c0 = (int)((int64_t)chunks * blockIdx.x / gridDim.x);

@@ -1,0 +1,48 @@
+"""Chunk attention and plans where they can go wrong: work smaller than the
+launch, NaN under short windows, pages freed behind a window, weights of very
+different sizes, flat attention over long contexts, captured plans.  The plain
+implementations and the tolerances are those of test_gpu_paged.py; where a test
+needs its own, it stands beside it."""
+
+import math
+
+import pytest
+import torch
+
+import sparse_dictionary_coded_b200 as sdk
+from test_gpu_paged import Case, _attend_ref, _i32, _status, _vec
+
+pytestmark = pytest.mark.gpu
+
+
+def _near(c, out, window=0):
+    d = c.q.shape[2]
+    want, tol, _, _ = _attend_ref(c.q, c.dk, c.dv, c.pages, c.table, c.lens, c.cu, True, window,
+                                  1 / math.sqrt(d))
+    return ((out.double() - want).abs() <= tol).all()
+
+
+# ------------------------------------------------- less work than the bounds
+
+@pytest.mark.parametrize("lens,window", [([50], 0), ([1], 0), ([3, 0, 2], 0), ([262144], 16),
+                                         ([262144], 64)], ids=str)
+def test_fewer_tokens_than_the_launch(lens, window):
+    """Few seen tokens in a call whose bounds admit many: results do not
+    depend on what the workspace held, finite or not, nor on an earlier call
+    over a longer context."""
+    new = [min(x, 1) for x in lens]
+    c = Case(lens, new, Hq=2, Hkv=1, n=32768, P=64, cols=4096, seed=21)
+    bounds = dict(max_q=1, max_len=262144, total=262144)
+    ws = c.workspace(**bounds)
+    got = []
+    for fill in (0, 0x3F800000, 0x7FC00000, 0x7F800000, -1):
+        ws[256:].view(torch.int32).fill_(fill)
+        lse = torch.full((c.q.shape[0], 2), 77.0, device="cuda")
+        got.append((c.run(window=window, ws=ws, lse=lse, **bounds), lse))
+    if window:
+        c.run(ws=ws, **bounds)                  # the whole context, and then again
+        got.append((c.run(window=window, ws=ws, lse=lse, **bounds), lse))
+    assert _status(ws) == (0, 0)
+    assert _near(c, got[0][0], window)
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
