@@ -488,13 +488,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // 2^x of two values, x <= 15, on the FMA units: x = n + f with n the nearest
 // integer (left in the low bits by adding 1.5 * 2^23), 2^f by a polynomial of
 // degree 3 fitted to the relative error on [-1/2, 1/2] with value 1 at 0
-// (at most 2^-13.2, a fifth of the fp16 rounding that follows), n added to
-// the exponent.  Below -127 the result is 0.
+// (at most 2^-13.3, a fifth of the fp16 rounding that follows), n added to
+// the exponent.  Below -127 the result is 0; NaN stays NaN: it passes the
+// clamp and comes back by the last addition of 0 x.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ void ex2_fma(uint64_t x2, float* y0, float* y1) {
   const float kBig = 12582912.0f;
   float a, b;
   unpack2(x2, &a, &b);
-  x2 = pack2(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
+  x2 = pack2(max_nan(a, -127.0f), max_nan(b, -127.0f));
   const uint64_t t = add2(x2, pack2(kBig, kBig));
   const uint64_t n = add2(t, pack2(-kBig, -kBig));
   const uint64_t f = fma2(n, pack2(-1.0f, -1.0f), x2);
@@ -504,8 +510,9 @@ __device__ __forceinline__ void ex2_fma(uint64_t x2, float* y0, float* y1) {
   float t0, t1, q0, q1;
   unpack2(t, &t0, &t1);
   unpack2(q, &q0, &q1);
-  *y0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
-  *y1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+  q0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+  q1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+  unpack2(fma2(x2, 0ull, pack2(q0, q1)), y0, y1);
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

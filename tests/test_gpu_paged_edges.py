@@ -46,3 +46,21 @@ def test_fewer_tokens_than_the_launch(lens, window):
     assert _near(c, got[0][0], window)
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+# --------------------------------------------------------------- NaN queries
+
+@pytest.mark.parametrize("window", [1, 2, 3])
+@pytest.mark.parametrize("lens,new", [([500, 900], [140, 1]), ([2000, 20], [4, 1]),
+                                      ([40000], [9])], ids=str)
+def test_nan_queries_under_short_windows(lens, new, window):
+    """A NaN query's row is NaN wherever its few seen tokens lie, its log-sum
+    too; the other rows are as before."""
+    c = Case(lens, new, seed=22)
+    want = c.run(window=window)
+    c.q[:, 2] = float("nan")
+    lse = torch.zeros(c.q.shape[:2], device="cuda")
+    got = c.run(window=window, lse=lse)
+    assert torch.isnan(got[:, 2]).all() and torch.isnan(lse[:, 2]).all()
+    keep = [h for h in range(8) if h != 2]
+    assert torch.equal(got[:, keep], want[:, keep]) and torch.isfinite(lse[:, keep]).all()
