@@ -413,7 +413,8 @@ SDK_API sdk_status sdk_decode_layout_of(int32_t B, int32_t Hq, int32_t head_dim,
  * from 1 to 65536.  A request's tokens lie in the pages of its row of
  *   block_table  int32 [B][max_pages]  page of tokens [c page_size,
  *                (c + 1) page_size) in column c; entries behind a request's
- *                last page are never read.
+ *                last page, and before the first token that a row of a call
+ *                sees (window), are never read.
  * Lengths are device arrays here (int32), so that a step can be planned,
  * captured and replayed without the host; what the host passes are bounds.
  * Conditions found on the device are recorded in the workspace header

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
     unsigned err;
     const ReqPlan rq = check_request(p, b, &err);
     const int t_tile = rq.lo + (tile - s_tile0[b]) * kTile;
-    const int t_end = rq.n > 0 ? rq.len : 0;
+    const int t_end = rq.n > 0 ? rq.len : 0, t_seen = first_seen(p, rq.len, rq.n);
     char* dst = tiles + ((int64_t)tile * p.Hkv + h) * (kTile * D * 2);
     const int r0 = part * kItemTok + warp * (TOK * TPS) + (rec >> 1);   // row of the tile
 #pragma unroll 1
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
       uint32_t w[WPL];
 #pragma unroll
       for (int i = 0; i < WPL; ++i) w[i] = 0u;
-      if (t < t_end) {
+      if (t >= t_seen && t < t_end) {   // (tokens before the first seen one are zero)
         const int col = t / p.page_size, off = t - col * p.page_size;
         const int page = p.table[(int64_t)b * p.max_pages + col];
         if (page >= 0 && page < p.n_pages) {

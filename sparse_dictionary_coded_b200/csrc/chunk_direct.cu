@@ -111,8 +111,7 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
     int lo = 0, units = 0;
     if (rq.n > 0) {
       // the first token any row sees, rounded down to a unit
-      const int seen = p.window > 0 ? max(rq.len - rq.n - p.window + 1, 0) : 0;
-      lo = min(seen, rq.len) / kUnit * kUnit;
+      lo = min(first_seen(p, rq.len, rq.n), rq.len) / kUnit * kUnit;
       units = max((rq.len - lo + kUnit - 1) / kUnit, 1);
     }
     s_req[tid] = make_int4(rq.row0, rq.n, rq.len, lo);
@@ -191,6 +190,7 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
     const int4 r4 = s_req[b];
     const int row0 = r4.x, n = r4.y, len = r4.z, rows = n * p.g;
     const int t_begin = r4.w + part * S * kUnit, t_end = min(len, t_begin + S * kUnit);
+    const int t_seen = first_seen(p, len, n);
     const int slot = parts > 1 ? before * p.Hkv + h * parts + part : -1;
     if (parts > 1 && part == 0 && tid == 0) {
       Split c;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kDirThreads, 2) chunk_direct_kernel(ChunkParam
         const int t = t0 + (i * kDirWarps + warp) * TPS + (rec >> 1);
 #pragma unroll
         for (int k = 0; k < WPL; ++k) w[i][k] = 0u;
-        if (t < t_end) {
+        if (t >= t_seen && t < t_end) {   // (tokens before the first seen one are zero)
           const int col = t / p.page_size, off = t - col * p.page_size;
           const int page = p.table[(int64_t)b * p.max_pages + col];
           if (page >= 0 && page < p.n_pages) {

@@ -6,7 +6,7 @@
 
 namespace sdk {
 
-constexpr int kTile = 128;   // tokens of a rebuilt tile; a request's first token rounds down to one
+constexpr int kTile = 128;   // tokens of a rebuilt tile; the first one a request sees rounds down to one
 constexpr int kRows = 256;   // packed rows of a block: two MMA tiles
 
 // Inclusive scan of one 64-bit value per thread (blockDim.x a multiple of
@@ -36,6 +36,13 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* s_warp, int6
   return r;
 }
 
+// The first token that a row of a request sees: its first row stands at len - n.
+// Tokens before it are neither looked up in the table nor read (their pages may
+// serve others by now).
+__device__ __forceinline__ int first_seen(const ChunkParams& p, int len, int n) {
+  return p.window > 0 ? (int)max((int64_t)len - n - p.window + 1, (int64_t)0) : 0;
+}
+
 // Checks request b's offsets and lengths; n = 0 refuses it (err says why).
 __device__ __forceinline__ ReqPlan check_request(const ChunkParams& p, int b, unsigned* err) {
   ReqPlan r = {};
@@ -50,9 +57,7 @@ __device__ __forceinline__ ReqPlan check_request(const ChunkParams& p, int b, un
   else
     r.n = row1 - r.row0;
   if (r.n > 0) {
-    // the first row's position len - n sees tokens from len - n - window + 1 on
-    if (p.window > 0) r.lo = (int)max((int64_t)r.len - r.n - p.window + 1, (int64_t)0);
-    r.lo = min(r.lo, r.len) / kTile * kTile;
+    r.lo = min(first_seen(p, r.len, r.n), r.len) / kTile * kTile;
     r.ntiles = (r.len - r.lo + kTile - 1) / kTile;
     r.npair = (int)(((int64_t)r.n * p.g + 1) / 2);
   }
@@ -81,6 +86,7 @@ __device__ void make_plan(const ChunkParams& p, bool leader, int32_t* s_first, i
     unsigned err = 0;
     ReqPlan r = {};
     if (b < p.B) r = check_request(p, b, &err);
+    if (ATOMS && r.n > 0) r.lo = min(first_seen(p, r.len, r.n), r.len);
     const int64_t units = ATOMS ? (int64_t)r.npair * p.Hkv : r.ntiles;
     int64_t tot_u, tot_w = 0;
     const int64_t upto = first + block_scan64(units, s_warp, &tot_u);

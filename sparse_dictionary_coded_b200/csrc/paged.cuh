@@ -35,7 +35,7 @@ struct ReqPlan {
   int row0;       // first row of q
   int n;          // new tokens (0: idle or refused)
   int len;        // tokens in the store
-  int lo;         // first token any row sees, rounded down to a tile
+  int lo;         // first token any row sees (by tiles: rounded down to one)
   int tile0;      // its first tile in the workspace
   int ntiles;
   int pair0;      // its first block of 256 packed rows (by atoms: first row pair)

@@ -64,3 +64,26 @@ def test_nan_queries_under_short_windows(lens, new, window):
     assert torch.isnan(got[:, 2]).all() and torch.isnan(lse[:, 2]).all()
     keep = [h for h in range(8) if h != 2]
     assert torch.equal(got[:, keep], want[:, keep]) and torch.isfinite(lse[:, keep]).all()
+
+
+# -------------------------------------------------------- pages behind a window
+
+@pytest.mark.parametrize("left", [-1, 1 << 30, "reused"], ids=str)
+@pytest.mark.parametrize("lens,new,kw,window", [
+    ([700], [129], dict(P=7), 50), ([1500] * 3, [90, 1, 40], dict(P=16, d=64), 200),
+    ([9000], [300], dict(P=24), 1000),
+    ([1100, 300], [3, 1], dict(P=16), 50), ([1100], [2], dict(P=1, d=64), 7),
+    ([40000], [1], dict(P=16, n=32768), 5001), ([40000, 900], [2, 1], dict(P=24, d=64), 3000)], ids=str)
+def test_pages_behind_the_window(lens, new, kw, window, left):
+    """Pages whose tokens no row sees any more may have left the table, or
+    serve others: they are neither looked up nor read."""
+    c = Case(lens, new, seed=23, **kw)
+    want = c.run(window=window)
+    if left == "reused":                        # a page of words that no call may use
+        left = (set(range(c.pages.shape[0])) - set(c.table.view(-1).tolist())).pop()
+    for b, (L, n) in enumerate(zip(lens, new)):
+        gone = max(0, L - n - window + 1) // c.P
+        assert gone > 0 or L < 1000
+        c.table[b, :gone] = left
+    ws = c.workspace()
+    assert torch.equal(c.run(window=window, ws=ws), want) and _status(ws) == (0, 0)
