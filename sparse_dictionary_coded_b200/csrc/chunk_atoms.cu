@@ -386,6 +386,15 @@ __device__ __forceinline__ uint4 load_words(const ChunkParams& p, uint32_t rec, 
   return __ldg(reinterpret_cast<const uint4*>(p.pages) + (int64_t)r * 8 + v * 4 + (lane & 3));
 }
 
+// Adds 2^x to the sum *z of terms over 2^*m, *m the largest x so far, with one
+// exponential; kNone: none yet (below every score, but -inf).
+constexpr float kNone = -3.4e38f;
+__device__ __forceinline__ void add_term(float x, float* m, float* z) {
+  const float d = x - *m, e = ex2(-fabsf(d));
+  *z = d > 0.0f ? fmaf(*z, e, 1.0f) : *z + e;
+  *m = fmaxf(*m, x);
+}
+
 template <typename F>
 __device__ __forceinline__ float block_reduce(float v, float zero, float* s_red, F f) {
 #pragma unroll
@@ -409,17 +418,17 @@ __device__ __forceinline__ uint32_t clean_word(uint32_t w, bool* bad) {
 
 // Adds p c of the segment's tokens [ta, ta + cnt) to the table for row e of
 // the pair, with m the row's maximum and `up` the fixed point.  Returns this
-// thread's part of sum_t p_t and of sum_t p_t sum_j |c_tj|.  CLEAN: bad words
-// are made harmless and recorded.  Tokens of no weight are not read.
+// thread's part of sum_t p_t sum_j |c_tj|.  CLEAN: bad words are made harmless
+// and recorded.  Tokens of no weight are not read.
 template <bool FULL, bool CLEAN>
-__device__ __forceinline__ float2 add_weights_of(const ChunkParams& p, uint32_t* tab,
-                                              const float2* score, const int32_t* table, int h,
-                                              int ta, int cnt, int e, float m, float up, int len,
-                                              int b) {
+__device__ __forceinline__ float add_weights_of(const ChunkParams& p, uint32_t* tab,
+                                                const float2* score, const int32_t* table, int h,
+                                                int ta, int cnt, int e, float m, float up, int len,
+                                                int b) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int own = (lane >> 2) + 8 * (lane & 3), mine = warp * 32 + own;
   const int P = p.page_size, dcol = kTokThreads / P, doff = kTokThreads - dcol * P;
-  float z = 0.0f, sum = 0.0f;
+  float sum = 0.0f;
   uint32_t top = 0u;
   auto score_of = [&](int u) {
     if (u >= cnt) return -INFINITY;
@@ -447,7 +456,6 @@ __device__ __forceinline__ float2 add_weights_of(const ChunkParams& p, uint32_t*
     s1 = score_of(u + own + 2 * kTokThreads);
     pg1 = page_of(table, at, u + own + 2 * kTokThreads < cnt);
     off1 = at.off;
-    z += w0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float pk = __shfl_sync(0xffffffffu, w0, (lane & ~3) | k);
@@ -473,22 +481,22 @@ __device__ __forceinline__ float2 add_weights_of(const ChunkParams& p, uint32_t*
   }
   if (!FULL && top >= (uint32_t)p.n)
     record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
-  return make_float2(z, sum);
+  return sum;
 }
 
 template <bool FULL>
-__device__ __forceinline__ float2 add_weights(const ChunkParams& p, uint32_t* tab,
-                                              const float2* score, const int32_t* table, int h,
-                                              int ta, int cnt, int e, float m, float up, int len,
-                                              int b) {
+__device__ __forceinline__ float add_weights(const ChunkParams& p, uint32_t* tab,
+                                             const float2* score, const int32_t* table, int h,
+                                             int ta, int cnt, int e, float m, float up, int len,
+                                             int b) {
   return add_weights_of<FULL, false>(p, tab, score, table, h, ta, cnt, e, m, up, len, b);
 }
 // the rare way, kept out of the loop's registers
 template <bool FULL>
-__device__ __forceinline__ float2 add_clean_weights(const ChunkParams& p, uint32_t* tab,
-                                                 const float2* score, const int32_t* table, int h,
-                                                 int ta, int cnt, int e, float m, float up, int len,
-                                                 int b) {
+__device__ __forceinline__ float add_clean_weights(const ChunkParams& p, uint32_t* tab,
+                                                   const float2* score, const int32_t* table, int h,
+                                                   int ta, int cnt, int e, float m, float up,
+                                                   int len, int b) {
   return add_weights_of<FULL, true>(p, tab, score, table, h, ta, cnt, e, m, up, len, b);
 }
 
@@ -501,10 +509,12 @@ __device__ __forceinline__ float2 add_clean_weights(const ChunkParams& p, uint32
 //      keeps the scores in the workspace; the segment's maxima follow.
 //   2. For each row the table becomes the weights: 16 integer additions a
 //      token, p c in fixed point.  Integer sums make the result independent
-//      of the order of the atomics.  The point is set from a sample of the
-//      segment's values with a margin; the exact bound sum_t p_t sum_j |c_tj|
-//      is summed up on the way, and the row is redone with the point it
-//      gives should the margin not have held.
+//      of the order of the atomics.  The point puts A = sum_t p_t sum_j |c_tj|,
+//      which bounds every atom's sum, near 10^9: A is estimated beforehand, as
+//      the exact sum_t p_t times the mean |c| of 640 tokens spread over the
+//      segment, weighted as they are; its exact value is summed up on the way,
+//      and the row is redone with that where the estimate was off by more
+//      than two: sums past 2^31 would wrap, small ones would lose bits.
 //   3. The weights are written as two bf16 parts (16 significand bits) in
 //      the layout the product with D_V reads.
 // Bound by the shared memory: random gathers and additions of 32 lanes need
@@ -514,8 +524,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     atoms_token_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ __align__(16) uint32_t tab[];   // [kTab]
   __shared__ float s_red[32];
-  __shared__ float s_sample[kTokThreads / 32][8];
-  __shared__ float s_bound[2];
+  __shared__ float s_sample[kTokThreads / 32][6];
+  __shared__ float s_bound[2], s_z[2];
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ uint32_t s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -597,7 +607,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     // ---- scores.  A warp takes 32 tokens at a time; four lanes read one
     // token's record (64 contiguous bytes), lane l ends with the sums of
     // token own(l) = l / 4 + 8 (l % 4).
-    float m0 = -INFINITY, m1 = -INFINITY;
+    float m0 = kNone, m1 = kNone, z0 = 0.0f, z1 = 0.0f;   // running maxima and sums of the lane's tokens
     bool nan0 = false, nan1 = false;
     uint32_t top = 0u;                        // largest atom index met
     // words one step ahead, pages two
@@ -672,8 +682,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         a1 = t >= see0[1] && t <= see1[1] ? a1 * sc1 : -INFINITY;
         nan0 |= a0 != a0;
         nan1 |= a1 != a1;
-        m0 = fmaxf(m0, a0);
-        m1 = fmaxf(m1, a1);
+        add_term(a0, &m0, &z0);
+        add_term(a1, &m1, &z1);
         score[t - ta] = make_float2(a0, a1);
       }
 #pragma unroll
@@ -683,18 +693,22 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     if (!FULL && top >= (uint32_t)p.n)
       record_error(p.hdr, SDK_ERR_DEVICE_CHECK, 0x77000000u | (uint32_t)b);
     const bool row_nan0 = __syncthreads_or(nan0) != 0, row_nan1 = __syncthreads_or(nan1) != 0;
-    m0 = block_reduce(m0, -INFINITY, s_red, fmax2);
-    m1 = block_reduce(m1, -INFINITY, s_red, fmax2);
+    const float q0 = block_reduce(m0, kNone, s_red, fmax2),
+                q1 = block_reduce(m1, kNone, s_red, fmax2);
+    z0 *= ex2(m0 - q0);
+    z1 *= ex2(m1 - q1);
+    m0 = q0 == kNone ? -INFINITY : q0;   // nothing seen
+    m1 = q1 == kNone ? -INFINITY : q1;
 
-    // ---- the size of p c from one token per thread; only tokens that a row
-    // sees have a say in its rounding
+    // ---- sum_t p_t, and the size of p c from one token per thread
     {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // per row: seen, |c|, p, p |c|
-      if (mine < cnt) {
-        const float2 s2 = score[mine];
-        at.init(ta + mine, P);
-        const float p0 = m0 > -INFINITY ? ex2(s2.x - m0) : 0.0f,
-                    p1 = m1 > -INFINITY ? ex2(s2.y - m1) : 0.0f;
+      float v[6] = {z0, 0.f, 0.f, z1, 0.f, 0.f};   // per row: sum of p; p and p |c| of the sample
+      const int sampled = min(cnt, kTokThreads);
+      if (tid < sampled) {
+        const int u = (int)((int64_t)tid * cnt / sampled);
+        const float2 s2 = score[u];
+        at.init(ta + u, P);
+        const float p0 = ex2(s2.x - q0), p1 = ex2(s2.y - q1);
         const bool in0 = p0 > 0.0f, in1 = p1 > 0.0f;             // (false for NaN)
         const uint32_t rec = record_of(p, page_of(table, at, true), at.off, h, in0 || in1, b);
         if (rec != kNoRecord) {
@@ -707,24 +721,24 @@ __global__ void __launch_bounds__(kTokThreads, 1)
           for (int k = 0; k < 4; ++k)
             a += (fabsf(word_coef(x[k].x)) + fabsf(word_coef(x[k].y))) +
                  (fabsf(word_coef(x[k].z)) + fabsf(word_coef(x[k].w)));
-          if (in0) v[0] = 1.0f, v[1] = a, v[2] = p0, v[3] = p0 * a;
-          if (in1) v[4] = 1.0f, v[5] = a, v[6] = p1, v[7] = p1 * a;
+          if (in0) v[1] = p0, v[2] = p0 * a;
+          if (in1) v[4] = p1, v[5] = p1 * a;
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 6; ++k)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
       if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s_sample[warp][k] = v[k];
+        for (int k = 0; k < 6; ++k) s_sample[warp][k] = v[k];
       __syncthreads();
       if (tid < 2) {
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
+        float t[3] = {0.f, 0.f, 0.f};
         for (int k = 0; k < kTokThreads / 32; ++k)
-          for (int q4 = 0; q4 < 4; ++q4) t[q4] += s_sample[k][4 * tid + q4];
-        const float seen = fmaxf(t[0], 1.0f), share = (float)cnt / (float)min(cnt, kTokThreads);
-        s_bound[tid] = 8.0f * fmaxf(t[1] / seen, fmaxf(t[3], t[2] * (t[1] / seen)) * share);
+          for (int i = 0; i < 3; ++i) t[i] += s_sample[k][3 * tid + i];
+        s_z[tid] = t[0];
+        s_bound[tid] = t[1] > 0.0f ? t[0] * (t[2] / t[1]) : 0.0f;
       }
       __syncthreads();
     }
@@ -744,39 +758,29 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                                : make_float2(-INFINITY, 0.0f);
         continue;
       }
-      float bound = s_bound[e];
-      float z = 0.0f, inv = 0.0f;
+      float bound = s_bound[e], inv = 0.0f;
       bool clean = false;
 #pragma unroll 1
       for (int attempt = 0; attempt < 3; ++attempt) {
-        // |w| <= bound: the point that puts bound below 2^30
-        if (!(bound > 1e-30f)) bound = 1e-30f;
-        if (!(bound < 1e30f)) bound = 1e30f;
-        const int ex = (int)((__float_as_uint(bound) >> 23) & 255u) - 127 + 1;   // bound < 2^ex
-        const float up = __uint_as_float((uint32_t)(min(30 - ex, 126) + 127) << 23);
+        // (an estimate from bad words may be anything)
+        const float up = 1.0e9f / fminf(fmaxf(bound, 1e-28f), 1e30f);
         inv = 1.0f / up;
         __syncthreads();
         for (int a = tid; a < kTab / 4; a += kTokThreads)
           reinterpret_cast<uint4*>(tab)[a] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        float za, aa;
-        const float2 sums =
+        const float mine_aa =
             clean ? add_clean_weights<FULL>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b)
                   : add_weights<FULL>(p, tab, score, table, h, ta, cnt, e, m, up, rp.len, b);
-        za = sums.x;
-        aa = sums.y;
-        z = block_reduce(za, 0.0f, s_red, fadd2);
-        aa = block_reduce(aa, 0.0f, s_red, fadd2);
-        if (aa * up < 2.0e9f) break;          // every sum fits (false for NaN)
-        if (!(aa < INFINITY)) {
-          clean = true;
-          bound = 0.0f;                       // the next attempt only finds the bound
-        } else {
-          bound = aa * 1.01f;
-        }
+        const float aa = block_reduce(mine_aa, 0.0f, s_red, fadd2);
+        if (aa * up < 2.0e9f && (aa * up > 5.0e8f || aa == 0.0f)) break;   // (false for NaN)
+        if (aa < INFINITY)
+          bound = aa;
+        else
+          clean = true;                       // a bad word; the third attempt knows A
       }
       __syncthreads();
-      if (tid == 0) p.part_ml[row] = make_float2(m, z);
+      if (tid == 0) p.part_ml[row] = make_float2(m, s_z[e]);
       // [row tile][chunk][part][128 rows][64 atoms], 128-byte swizzle
       const int chunks = (p.n + kChunk - 1) / kChunk;
       char* img = p.wimg + (int64_t)(row / kN) * chunks * 2 * (kN * 128) + (row % kN) * 128;

@@ -87,3 +87,28 @@ def test_pages_behind_the_window(lens, new, kw, window, left):
         c.table[b, :gone] = left
     ws = c.workspace()
     assert torch.equal(c.run(window=window, ws=ws), want) and _status(ws) == (0, 0)
+
+
+# --------------------------------------------------- sizes of weights by atoms
+
+@pytest.mark.parametrize("where", [[5, 900, 39990], [39999], [20000, 20001, 20002, 20003]], ids=str)
+def test_heavy_tokens_with_small_values(where):
+    """A few tokens have all the weight and values a ten-millionth of the others'
+    (whose probabilities are below 2^-50): the weights keep their bits."""
+    c = Case([40000], [1], Hq=4, Hkv=2, n=5000, seed=24)
+    half = lambda x: x.clamp(-65504, 65504).half().view(torch.int16).to(torch.int32) << 16
+    times = lambda w, f: half((w >> 16).to(torch.int16).view(torch.float16).float() * f) | (w & 0x7FFF)
+    k, v = c.pages[:, :, :, 0], c.pages[:, :, :, 1]
+    good = ((k[..., 0] & 0x7FFF) < 5000)[..., None]           # slots that hold a token
+    c.pages[:, :, :, 0] = torch.where(good, times(k, 1e-4), k)
+    c.pages[:, :, :, 1] = torch.where(good, times(v, 2e4), v)
+    c.q[:] = c.q[:, :1]
+    for h in range(2):
+        row = c.q[0, 2 * h].double() @ c.dk.double().T / math.sqrt(128)
+        atom = int(row.argmax())
+        word = half(40.0 / row[atom].float()).item() | atom    # a score of 40: e^40 = 2^57
+        for t in where:
+            page, off = c.table[0, t // c.P].item(), t % c.P
+            c.pages[page, h, off, 0, 0] = word
+            c.pages[page, h, off, 1] = times(c.pages[page, h, off, 1], 1e-7)
+    c.check()
