@@ -520,8 +520,10 @@ SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dt
  *   requests' contents, but their last bits may on how the batch cuts the
  *   contexts.  The host's bounds choose the form: tight ones choose better.
  * Arithmetic: rebuilt vectors and probabilities (by atoms: <q, D_K>) enter
- *   the products in fp16 (fp32 sums), weights per atom with 16 significand
- *   bits; q exactly.  A rebuilt entry beyond +-65504 or NaN is recorded
+ *   the products in fp16 (fp32 sums); q enters exactly.  By atoms, a product
+ *   p c is rounded to a multiple of at most 2^-28 of the sum of |p c| over a
+ *   share of at most 32768 tokens (on average 3e-4 of a product where all
+ *   tokens weigh the same), and an atom's weight to 16 significand bits.  A rebuilt entry beyond +-65504 or NaN is recorded
  *   (SDK_ERR_DEVICE_CHECK) and taken as +-65504 or 0; below 2^-14 it keeps an
  *   absolute error of 2^-25, as the coefficients themselves do.  So is, by
  *   atoms, an infinite or NaN coefficient; a code word whose atom is not in

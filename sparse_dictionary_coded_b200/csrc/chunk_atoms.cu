@@ -21,18 +21,26 @@ constexpr int kN = 128;            // rows per MMA tile
 constexpr int kM = 128;            // atoms per QD tile, head dims of w D_V
 constexpr int kChunk = 64;         // atoms per step of w D_V
 constexpr int kTab = SDK_MAX_ATOMS;
-constexpr int kMaxCtas = 512;      // CTAs of the token kernel
+constexpr int64_t kShareTokens = 1 << 15;   // tokens of a share at most
+// segments of a pair at most: shares are longer than half of kShareTokens
+// where there are more of them than SMs
+constexpr int kMaxSegs = 2 * (int)(kAtomsMaxLen / kShareTokens) + 2;
 constexpr int kTokThreads = 640;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Shares that `work` units are cut into, none of them empty: of a thousand
-// tokens at least (fewer would leave threads idle), `most` of them at most.
-// The host sizes the launch by the bound on the work, the device cuts the work
-// there is: a share without a unit would leave its sums unwritten.
-__host__ __device__ __forceinline__ int share_count(int64_t work, int most) {
-  const int64_t want = work / 1024;
-  return (int)(want < 1 ? 1 : want > most ? most : want);
+// tokens at least (fewer would leave threads idle), one per SM, or as many for
+// every SM as keep them within kShareTokens.  The host sizes the launch by the
+// bound on the work, the device cuts the work there is: a share without a unit
+// would leave its sums unwritten.
+// A product p c is rounded to a unit of at most A / 5e8 (A = sum_t p_t sum_j
+// |c_tj| over the share), so over S flat tokens its deviation is 9e-9 S of the
+// mean product: 3e-4 at 2^15 tokens, below the 1e-3 that bf16 outputs have
+// anyhow (without the bound 2e-3 at four requests of 262144).
+__host__ __device__ __forceinline__ int share_count(int64_t work, int sms) {
+  const int64_t want = work / 1024, rounds = (work + sms * kShareTokens - 1) / (sms * kShareTokens);
+  return (int)(want < 1 ? 1 : want < sms ? want : sms * rounds);
 }
 
 struct AtomCut {
@@ -51,7 +59,7 @@ AtomCut atom_cut(int B, int64_t n_tok, int Hq, int Hkv, int n, int max_q, int ma
   int64_t tokens = (int64_t)B * max_len;
   if (total_len > 0 && total_len < tokens) tokens = total_len;
   c.work = tokens * Hkv * each;
-  c.ctas = share_count(c.work, num_sms() < kMaxCtas ? num_sms() : kMaxCtas);
+  c.ctas = share_count(c.work, num_sms());
   // a segment is a CTA's share of one pair: at most ctas + pairs of them
   c.row_tiles = (int)((2 * (c.ctas + c.pairs) + kN - 1) / kN);
   c.chunks = (n + kChunk - 1) / kChunk;
@@ -502,8 +510,8 @@ __device__ __forceinline__ float add_clean_weights(const ChunkParams& p, uint32_
 
 }  // namespace
 
-// One CTA per SM takes an equal share of the (row pair, token) units, cut
-// into segments of one pair.  Per segment:
+// A CTA, one at a time on an SM, takes an equal share of the (row pair, token)
+// units, cut into segments of one pair.  Per segment:
 //   1. QD of the pair (fp16, 128 KB) is copied to shared memory; a thread
 //      per token adds up 16 gathered products for both rows at once and
 //      keeps the scores in the workspace; the segment's maxima follow.
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   pdl_launch();
   pdl_wait();
   const int64_t W = p.plan[p.B].work0;
-  const int shares = share_count(W, p.ctas);
+  const int shares = share_count(W, p.sms);
   if (W == 0 || (int)blockIdx.x >= shares) return;
   int64_t w = W * blockIdx.x / shares;
   const int64_t w_end = W * (blockIdx.x + 1) / shares;
@@ -593,6 +601,24 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       see0[e] = p.window > 0 ? pos - p.window + 1 : 0;
     }
     const float sc0 = p.row_scale[2 * pair], sc1 = p.row_scale[2 * pair + 1];
+    // sum_j |c_j| of the thread's sample of the values, on its way while QD is
+    const int sampled = min(cnt, kTokThreads), sample = (int)((int64_t)tid * cnt / sampled);
+    float sample_c = 0.0f;
+    PageAt at;
+    if (tid < sampled) {
+      at.init(ta + sample, P);
+      const uint32_t rec = record_of(p, page_of(table, at, true), at.off, h, true, b);
+      if (rec != kNoRecord) {
+        const uint4* words = reinterpret_cast<const uint4*>(p.pages) + (int64_t)rec * 8 + 4;
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = __ldg(words + k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sample_c += (fabsf(word_coef(x[k].x)) + fabsf(word_coef(x[k].y))) +
+                      (fabsf(word_coef(x[k].z)) + fabsf(word_coef(x[k].w)));
+      }
+    }
     const bool got = tc::mbar_wait(tc::smem_u32(&s_bar), parity, &s_abort);
     parity ^= 1u;
     if (!__syncthreads_and(got)) {
@@ -611,7 +637,6 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     bool nan0 = false, nan1 = false;
     uint32_t top = 0u;                        // largest atom index met
     // words one step ahead, pages two
-    PageAt at;
     at.init(min(ta + mine, rp.len), P);
     uint4 x[4], y[4];
     uint32_t rec = record_of(p, page_of(table, at, mine < cnt), at.off, h, mine < cnt, b);
@@ -703,27 +728,11 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     // ---- sum_t p_t, and the size of p c from one token per thread
     {
       float v[6] = {z0, 0.f, 0.f, z1, 0.f, 0.f};   // per row: sum of p; p and p |c| of the sample
-      const int sampled = min(cnt, kTokThreads);
       if (tid < sampled) {
-        const int u = (int)((int64_t)tid * cnt / sampled);
-        const float2 s2 = score[u];
-        at.init(ta + u, P);
+        const float2 s2 = score[sample];
         const float p0 = ex2(s2.x - q0), p1 = ex2(s2.y - q1);
-        const bool in0 = p0 > 0.0f, in1 = p1 > 0.0f;             // (false for NaN)
-        const uint32_t rec = record_of(p, page_of(table, at, true), at.off, h, in0 || in1, b);
-        if (rec != kNoRecord) {
-          const uint4* words = reinterpret_cast<const uint4*>(p.pages) + (int64_t)rec * 8 + 4;
-          uint4 x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = __ldg(words + k);
-          float a = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            a += (fabsf(word_coef(x[k].x)) + fabsf(word_coef(x[k].y))) +
-                 (fabsf(word_coef(x[k].z)) + fabsf(word_coef(x[k].w)));
-          if (in0) v[1] = p0, v[2] = p0 * a;
-          if (in1) v[4] = p1, v[5] = p1 * a;
-        }
+        if (p0 > 0.0f) v[1] = p0, v[2] = p0 * sample_c;            // (not for NaN)
+        if (p1 > 0.0f) v[4] = p1, v[5] = p1 * sample_c;
       }
 #pragma unroll
       for (int k = 0; k < 6; ++k)
@@ -847,7 +856,7 @@ __global__ void __launch_bounds__(128, 1)
   pdl_launch();
   pdl_wait();
   // rows that no segment wrote are not read
-  const int rows = 2 * (share_count(p.plan[p.B].work0, p.ctas) + p.plan[p.B].pair0);
+  const int rows = 2 * (share_count(p.plan[p.B].work0, p.sms) + p.plan[p.B].pair0);
   if ((int)blockIdx.y * kN >= rows) return;
   const int chunks = (p.n + kChunk - 1) / kChunk;
   const int c0 = (int)((int64_t)chunks * blockIdx.x / gridDim.x);
@@ -961,7 +970,7 @@ template <int D>
 __global__ void __launch_bounds__(512) atoms_join_kernel(ChunkParams p) {
   constexpr int G = 16;
   __shared__ float s_o[512];
-  __shared__ float2 s_ml[kMaxCtas];
+  __shared__ float2 s_ml[kMaxSegs];
   pdl_wait();
   const int pair = (int)blockIdx.x / (2 * (D / 32)), e = (int)blockIdx.x / (D / 32) & 1;
   const int4 of = p.pair_of[pair];                 // (of a pair that is not there: not used)
@@ -1060,6 +1069,7 @@ sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
   p.cap_pairs = c.pairs;
   p.cap_work = c.work;
   p.ctas = c.ctas;
+  p.sms = num_sms();
   p.row_tiles = c.row_tiles;
   p.ksplits = c.ksplits;
   p.n_pad = c.n_pad;

@@ -1164,9 +1164,8 @@ static Form pick_form(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int m
   const double atoms = 30 + 7e-5 * T + 4e-5 * T * pairs + 9.0 * n / SDK_MAX_ATOMS +
                        (15 + 22.0 * n / SDK_MAX_ATOMS) * all / num_sms();
   const bool one_pass = direct_fits(B, n_tok, (int)g, max_q, max_len) && direct < tiles;
-  // by atoms, an atom's sum over a share's tokens has to fit 32 bits with its
-  // roundings (half a unit, 16 words a token), and the pairs fit a grid
-  if (min((double)max_len, T * pairs / num_sms()) <= (double)(1 << 24) && all <= (double)(1 << 21) &&
+  // by atoms, the pairs and the shares have to fit a grid, a pair's segments its join
+  if (max_len <= kAtomsMaxLen && all <= (double)kAtomsMaxPairs && T * pairs <= (double)kAtomsMaxWork &&
       atoms < (one_pass ? direct : tiles))
     return Form::atoms;
   return one_pass ? Form::direct : Form::tiles;

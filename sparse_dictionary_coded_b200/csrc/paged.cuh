@@ -75,7 +75,7 @@ struct ChunkParams {
   int64_t n_tok, cap_pairs, cap_work;
   int B, Hq, Hkv, g, d, n, n_pad, n_pages, page_size, max_pages;
   int max_q, max_len, window, causal, cap_tiles;
-  int ctas, whole, parts, ksplits, row_tiles;
+  int ctas, sms, whole, parts, ksplits, row_tiles;
   float scale;
 };
 
@@ -84,7 +84,10 @@ sdk_status launch_paged_store(const StoreParams& p, cudaStream_t stream);
 // total_len as the caller's (0: B * max_len)
 sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
                              cudaStream_t stream);
-// the other two forms (chunk_atoms.cu, chunk_direct.cu)
+// the other two forms (chunk_atoms.cu, chunk_direct.cu); by atoms: contexts of
+// at most kAtomsMaxLen tokens, kAtomsMaxPairs row pairs over all KV heads and
+// kAtomsMaxWork (row pair, token) units
+constexpr int64_t kAtomsMaxLen = 1 << 24, kAtomsMaxPairs = 1 << 21, kAtomsMaxWork = (int64_t)1 << 35;
 size_t atoms_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len);
 sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,

@@ -112,3 +112,57 @@ def test_heavy_tokens_with_small_values(where):
             c.pages[page, h, off, 0, 0] = word
             c.pages[page, h, off, 1] = times(c.pages[page, h, off, 1], 1e-7)
     c.check()
+
+
+# -------------------------------------------------- flat long contexts by atoms
+
+def test_flat_attention_over_long_contexts():
+    """2.4 million tokens, all of the same weight: sums that cancel keep their
+    bits however many tokens an SM adds up.
+
+    Tolerance: an output is a sum of N = 2.4e6 x 16 products of random signs;
+    with r its root mean square over rows and dims,
+        |out - ref| <= 2^-8 |ref| (bf16) + 1.9e-3 r.
+    A product p c is rounded to a multiple of a unit u that is at most
+    sum |p c| / 5e8 of its share of S <= 2^15 tokens, that is 16 S mean|pc| / 5e8
+    = 1.05e-3 mean|pc|; a rounding's deviation is u / sqrt(12) = 3.0e-4 mean|pc|,
+    against sqrt(pi / 2) mean|pc| of the product: 2.4e-4 r after the same sum;
+    4096 outputs stay within six deviations: 1.5e-3 r.  The scale of 1e-6 keeps
+    scores below 1e-4, known to 1e-4 2^-11, so that even a sum of errors of one
+    sign is below 5e-8 / (mean / rms of the sum: 1 / sqrt(N)) = 3e-4 r.  Weights
+    as two bf16 parts (2^-17) and fp32 sums add less than 1e-4 r."""
+    L, Hkv, Hq, d, n, P = 2400000, 2, 32, 128, 32768, 64
+    g = torch.Generator(device="cuda").manual_seed(25)
+    n_pages = L // P
+    pages = torch.empty(n_pages, Hkv, P, 2, 16, dtype=torch.int32, device="cuda")
+    for i in range(0, n_pages, 5000):
+        k = min(5000, n_pages - i)
+        idx = torch.randint(0, n, (k, Hkv, P, 2, 16), generator=g, device="cuda", dtype=torch.int32)
+        c = torch.randn(idx.shape, generator=g, device="cuda").half()
+        pages[i:i + k] = (c.view(torch.int16).to(torch.int32) << 16) | idx
+    D = torch.randn(2, n, d, generator=g, device="cuda")
+    D = (D / D.norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+    q = (torch.randn(1, Hq, d, generator=g, device="cuda") * 2).to(torch.bfloat16)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    ws = sdk.new_workspace(sdk.sdk_chunk_attn_workspace_bytes(1, 1, Hq, Hkv, d, n, 1, L, L))
+    out = sdk.sdk_chunk_attn(q, D[0].contiguous(), D[1].contiguous(), pages, table, _i32([L]),
+                             _i32([0, 1]), 1, L, total_len=L, scale=1e-6, workspace=ws)
+    assert _status(ws) == (0, 0)
+    ref = torch.empty(Hq, d, dtype=torch.float64, device="cuda")
+    for h in range(Hkv):
+        rec = pages[:, h].reshape(L, 2, 16)
+        coef = (rec >> 16).to(torch.int16).view(torch.float16)
+        idx = (rec & 0x7FFF).long()
+        for r in range(h * 16, h * 16 + 16):
+            qd = D[0].double() @ q[0, r].double()
+            s = torch.zeros(L, dtype=torch.float64, device="cuda")
+            for j in range(16):
+                s += coef[:, 0, j].double() * qd[idx[:, 0, j]]
+            p = torch.softmax(s * 1e-6, 0)
+            w = torch.zeros(n, dtype=torch.float64, device="cuda")
+            for j in range(16):
+                w.index_add_(0, idx[:, 1, j], p * coef[:, 1, j].double())
+            ref[r] = w @ D[1].double()
+    err, r = (out[0].double() - ref).abs(), ref.square().mean().sqrt()
+    far = err - (2.0 ** -8 * ref.abs() + 1.9e-3 * r)
+    assert not (far > 0).any(), "over by %g r at %d places" % (far.max() / r, (far > 0).sum())
