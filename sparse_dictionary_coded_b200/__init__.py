@@ -485,11 +485,15 @@ class PagedCodeStore:
 
     def plan(self, lens, n_new, block_table, max_new, workspace=None, stream=None):
         """sdk_block_tables over this pool's free pages; the stack then holds
-        what is left (a new n_free tensor replaces the old one)."""
+        what is left.  free_pages and n_free stay where they are, so a plan
+        captured in a CUDA graph takes other pages with every replay."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.plan(lens, n_new, block_table, max_new, workspace)
         r = sdk_block_tables(lens, n_new, self.free_pages, self.n_free, block_table,
                              self.page_size, max_new, n_pages=self.n_pages,
-                             workspace=workspace, stream=stream)
-        self.n_free = r.n_free
+                             workspace=workspace)
+        self.n_free.copy_(r.n_free)
         return r
 
     def release(self, page_ids):
@@ -499,4 +503,4 @@ class PagedCodeStore:
         n = page_ids.numel()
         at = self.n_free.long() + torch.arange(n, device=self.free_pages.device)
         self._room[at.clamp(max=self.n_pages)] = page_ids.to(torch.int32)
-        self.n_free = (self.n_free + n).clamp(max=self.n_pages)
+        self.n_free.add_(n).clamp_(max=self.n_pages)

@@ -166,3 +166,37 @@ def test_flat_attention_over_long_contexts():
     err, r = (out[0].double() - ref).abs(), ref.square().mean().sqrt()
     far = err - (2.0 ** -8 * ref.abs() + 1.9e-3 * r)
     assert not (far > 0).any(), "over by %g r at %d places" % (far.max() / r, (far > 0).sum())
+
+
+# ------------------------------------------------------------- captured plans
+
+def test_plan_replays_on_its_pool():
+    """PagedCodeStore.plan captured in a graph: every replay takes pages of
+    its own, releases between replays are seen, and a plan without a graph
+    goes on where the replays ended."""
+    store = sdk.PagedCodeStore(12, 1, 4)
+    lens, new, table = _i32([0, 0]), _i32([4, 8]), _i32([[-1] * 8] * 2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        store.plan(_i32([0]), _i32([0]), _i32([[-1]]), 1)      # nothing is taken
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = store.plan(lens, new, table, 12)
+        lens.copy_(plan.new_lens)
+    for k in (1, 2):
+        graph.replay()
+        assert lens.tolist() == [4 * k, 8 * k] and store.n_free.tolist() == [12 - 3 * k]
+        assert plan.n_free.tolist() == [12 - 3 * k]
+    held = table[0, :2].tolist() + table[1, :4].tolist()
+    assert sorted(held) == list(range(6))
+    store.release(table[1, :4].clone())
+    assert store.n_free.tolist() == [10]
+    lens.copy_(_i32([8, 0]))
+    graph.replay()
+    assert store.n_free.tolist() == [7] and lens.tolist() == [12, 8]
+    plan = store.plan(lens, new, table, 12)
+    assert store.n_free.tolist() == [4] and plan.n_free.tolist() == [4]
+    held = table[0, :4].tolist() + table[1, :4].tolist()
+    assert len(set(held)) == 8
