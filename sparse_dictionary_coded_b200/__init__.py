@@ -366,8 +366,11 @@ def sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size,
     [B, max_pages]; max_new: rows of the slot map (a bound on the step's
     tokens).  n_pages: pages of the pool (default: the length of
     free_pages, which may hold fewer entries than the pool has pages).
-    Returns BlockTables, its new tensors in one buffer; requests that do not
-    fit are refused and recorded in the workspace (include/sdk.h)."""
+    Returns BlockTables, its new tensors in one buffer.  Requests that do not
+    fit are refused (include/sdk.h): their slots are -1, their new_lens are
+    their lens, and their rows must be left out of what follows.  Give a
+    workspace to learn of it (sdk_check_status); one made here goes with the
+    call."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size, max_new,
@@ -389,7 +392,8 @@ def sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace=None,
     """Writes the code words codes_k, codes_v int32 [n_tok, Hkv, 16] (or
     [n_tok * Hkv, 16], as sdk_encode returns them) to their slots of pages
     int32 [n_pages, Hkv, page_size, 2, 16]; slot_map int64 [n_tok], negative
-    slots are skipped.  Returns pages."""
+    slots are skipped, slots past the pool recorded in the workspace (give one
+    to see it).  Returns pages."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace)
@@ -450,7 +454,12 @@ def sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q,
     total_len are host bounds on the new tokens and the context of a request
     and on all contexts together (0: B * max_len).  Returns out bf16 [n_tok,
     Hq, head_dim]; lse: a float32 [n_tok, Hq] tensor that receives the
-    logarithms of the softmax sums."""
+    logarithms of the softmax sums.
+
+    Rows of no request, and those of a request that the device refuses, are
+    left as they were in out and lse; in an out made here they hold whatever
+    its memory held.  Give a workspace to learn of refusals and bad pages
+    (sdk_check_status); the record of one made here goes with the call."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q, max_len,
@@ -472,6 +481,9 @@ class PagedCodeStore:
         sdk_paged_append(store.pages, xk, xv, dict_k, dict_v, plan.slot_map)
         out = sdk_chunk_attn(q, dict_k, dict_v, store.pages, block_table,
                              plan.new_lens, plan.cu_new, max_q, max_len)
+
+    workspace records the refusals of plans that were given none:
+    sdk_check_status(store.workspace) is not SDK_OK when a request did not fit.
     """
 
     def __init__(self, n_pages, Hkv, page_size, device="cuda"):
@@ -482,6 +494,8 @@ class PagedCodeStore:
         self._room = torch.arange(n_pages - 1, -2, -1, dtype=torch.int32, device=device)
         self.free_pages = self._room[:n_pages]
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        with torch.cuda.device(self.n_free.device):
+            self.workspace = new_workspace(sdk_block_tables_workspace_bytes(1), self.n_free.device)
 
     def plan(self, lens, n_new, block_table, max_new, workspace=None, stream=None):
         """sdk_block_tables over this pool's free pages; the stack then holds
@@ -492,7 +506,7 @@ class PagedCodeStore:
                 return self.plan(lens, n_new, block_table, max_new, workspace)
         r = sdk_block_tables(lens, n_new, self.free_pages, self.n_free, block_table,
                              self.page_size, max_new, n_pages=self.n_pages,
-                             workspace=workspace)
+                             workspace=self.workspace if workspace is None else workspace)
         self.n_free.copy_(r.n_free)
         return r
 

@@ -200,3 +200,19 @@ def test_plan_replays_on_its_pool():
     assert store.n_free.tolist() == [4] and plan.n_free.tolist() == [4]
     held = table[0, :4].tolist() + table[1, :4].tolist()
     assert len(set(held)) == 8
+
+
+# ------------------------------------------------------------ records of plans
+
+def test_refusals_are_kept_by_the_store():
+    """A plan without a workspace records in the store's, until it is read."""
+    store = sdk.PagedCodeStore(3, 1, 4)
+    table = _i32([[-1] * 4] * 2)
+    plan = store.plan(_i32([0, 0]), _i32([4, 9]), table, 13)         # four pages of three
+    assert plan.new_lens.tolist() == [4, 0] and plan.cu_new.tolist() == [0, 4, 13]
+    assert plan.slot_map.tolist() == [0, 1, 2, 3] + [-1] * 9
+    store.plan(_i32([4, 0]), _i32([1, 0]), table, 1)
+    assert _status(store.workspace)[0] == 3 and _status(store.workspace)[0] == 0
+    ws = sdk.new_workspace(256)
+    store.plan(_i32([5, 0]), _i32([0, 9]), table, 9, workspace=ws)
+    assert _status(store.workspace)[0] == 0 and _status(ws)[0] == 3
