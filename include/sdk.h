@@ -442,11 +442,17 @@ SDK_API sdk_status sdk_decode_layout_of(int32_t B, int32_t Hq, int32_t head_dim,
  *   new_lens     device, int32 [B]: L + n (L for a refused request)
  *   n_free_out   device, int32 [1]: pages left
  * A request is refused as a whole, and takes no page, when L + n needs more
- * than max_pages columns, when its rows pass max_new, when the pages up to
- * and including its own exceed n_free[0] (SDK_ERR_CAPACITY), or when L or n
- * is negative or L + n passes 2^31 - 1 (SDK_ERR_DEVICE_CHECK).  The outputs
- * must not overlap the inputs (SDK_ERR_INVALID_ARG): the call changes none
- * of its inputs but the table, so repeating it gives the same plan.
+ * than max_pages columns, when its rows pass max_new, when it needs pages and
+ * those up to and including its own exceed n_free[0] (SDK_ERR_CAPACITY; a
+ * request behind it that needs none goes on), or when L or n is negative or
+ * L + n passes 2^31 - 1 (SDK_ERR_DEVICE_CHECK).  A refused request keeps its
+ * rows in cu_new, with slots of -1, and its length: nothing is stored for
+ * them, and sdk_chunk_attn, which sees n rows and L tokens, answers them as
+ * the rows at L - n .. L - 1.  Leave them out of what follows (new_lens !=
+ * lens + n_new says which) and plan the request again when pages are free.
+ * The outputs must not overlap the inputs (SDK_ERR_INVALID_ARG): the call
+ * changes none of its inputs but the table, so repeating it gives the same
+ * plan.
  */
 SDK_API size_t sdk_block_tables_workspace_bytes(int32_t B);
 SDK_API sdk_status sdk_block_tables(const int32_t* lens, const int32_t* n_new, int32_t B,
@@ -523,13 +529,14 @@ SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dt
  *   the products in fp16 (fp32 sums); q enters exactly.  By atoms, a product
  *   p c is rounded to a multiple of at most 2^-28 of the sum of |p c| over a
  *   share of at most 32768 tokens (on average 3e-4 of a product where all
- *   tokens weigh the same), and an atom's weight to 16 significand bits.  A rebuilt entry beyond +-65504 or NaN is recorded
- *   (SDK_ERR_DEVICE_CHECK) and taken as +-65504 or 0; below 2^-14 it keeps an
- *   absolute error of 2^-25, as the coefficients themselves do.  So is, by
- *   atoms, an infinite or NaN coefficient; a code word whose atom is not in
- *   the dictionary is recorded and counts as 0.  By atoms, a value's words
- *   are examined where a row gives its token weight, and <q, D_K> stays in
- *   range for atoms of norms up to 2900.
+ *   tokens weigh the same), and an atom's weight to 16 significand bits.  A
+ *   rebuilt entry beyond +-65504 or NaN is recorded (SDK_ERR_DEVICE_CHECK) and
+ *   taken as +-65504 or 0; below 2^-14 it keeps an absolute error of 2^-25, as
+ *   the coefficients themselves do.  So is, by atoms, an infinite or NaN
+ *   coefficient; a code word whose atom is not in the dictionary is recorded
+ *   and counts as 0.  By atoms, a value's words are examined where a row gives
+ *   its token weight, and <q, D_K> stays in range for atoms of norms up to
+ *   2900.
  * A request whose cu_q, n or len lies outside its bounds is refused:
  *   recorded, its rows are not touched.
  */

@@ -216,3 +216,29 @@ def test_refusals_are_kept_by_the_store():
     ws = sdk.new_workspace(256)
     store.plan(_i32([5, 0]), _i32([0, 9]), table, 9, workspace=ws)
     assert _status(store.workspace)[0] == 0 and _status(ws)[0] == 3
+
+
+# ------------------------------------------------------------- refused requests
+
+def test_a_refused_request_leaves_the_others():
+    """The pool runs out at the second of four requests: the third needs a
+    page and is refused too, the fourth needs none and goes on.  The accepted
+    ones' slots and rows are those of a step without the others."""
+    c = Case([20, 30, 16, 5], [2, 1, 1, 1], P=16, n=100, cols=4, seed=26)
+    lens, new = _i32([18, 32, 16, 4]), _i32([2, 20, 3, 1])
+    free = _i32([c.pages.shape[0] - 1])
+    r = sdk.sdk_block_tables(lens, new, free, _i32([1]), c.table.clone(), 16, 26,
+                             n_pages=c.pages.shape[0])
+    assert r.new_lens.tolist() == [20, 32, 16, 5] and r.cu_new.tolist() == [0, 2, 22, 25, 26]
+    assert r.n_free.tolist() == [1] and r.block_table.tolist() == c.table.tolist()
+    assert (r.new_lens != lens + new).tolist() == [False, True, True, False]
+    slots = r.slot_map.tolist()
+    assert slots[2:25] == [-1] * 23
+    at = lambda b, t: c.table[b, t // 16].item() * 16 + t % 16
+    assert slots[:2] == [at(0, 18), at(0, 19)] and slots[25] == at(3, 4)
+    q = c.q[:1].expand(26, -1, -1).contiguous()
+    q[:2], q[25] = c.q[:2], c.q[4]
+    out = sdk.sdk_chunk_attn(q, c.dk, c.dv, c.pages, c.table, r.new_lens, r.cu_new, 20, 32)
+    want, tol, _, _ = _attend_ref(c.q, c.dk, c.dv, c.pages, c.table, c.lens, c.cu, True, 0,
+                                  1 / math.sqrt(128))
+    assert ((out[[0, 1, 25]].double() - want[[0, 1, 4]]).abs() <= tol[[0, 1, 4]]).all()
