@@ -1047,10 +1047,9 @@ static sdk_status launch_atoms_d(const CUtensorMap& kmap, const CUtensorMap& vma
 }
 
 sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
-                              cudaStream_t stream, bool* taken) {
-  *taken = false;
+                              cudaStream_t stream) {
   auto fn = tc::encode_fn();
-  if (fn == nullptr) return SDK_OK;
+  if (fn == nullptr) return SDK_ERR_CUDA;
   CUtensorMap maps[2];
   for (int s = 0; s < 2; ++s) {
     const cuuint64_t dims[2] = {(cuuint64_t)p.d, (cuuint64_t)p.n};
@@ -1061,9 +1060,8 @@ sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
            const_cast<uint16_t*>(s == 0 ? p.dk : p.dv), dims, strides, box, estr,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return SDK_OK;
+      return SDK_ERR_CUDA;
   }
-  *taken = true;
   const AtomCut c = atom_cut(p.B, p.n_tok, p.Hq, p.Hkv, p.n, p.max_q, p.max_len, total_len);
   const AtomLayout l = atom_layout(p.B, p.d, c);
   p.cap_pairs = c.pairs;

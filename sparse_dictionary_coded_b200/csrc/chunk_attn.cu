@@ -1166,7 +1166,7 @@ static Form pick_form(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int m
   const bool one_pass = direct_fits(B, n_tok, (int)g, max_q, max_len) && direct < tiles;
   // by atoms, the pairs and the shares have to fit a grid, a pair's segments its join
   if (max_len <= kAtomsMaxLen && all <= (double)kAtomsMaxPairs && T * pairs <= (double)kAtomsMaxWork &&
-      atoms < (one_pass ? direct : tiles))
+      atoms < (one_pass ? direct : tiles) && tc::encode_fn() != nullptr)
     return Form::atoms;
   return one_pass ? Form::direct : Form::tiles;
 }
@@ -1205,15 +1205,13 @@ size_t chunk_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n
   const Form form = pick_form(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
   if (form == Form::direct)
     return direct_workspace_bytes(B, n_tok, Hq, Hkv, d, max_q, max_len, total_len);
+  if (form == Form::atoms)
+    return atoms_workspace_bytes(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
   const int64_t q = max_q < n_tok ? max_q : n_tok;
   const int64_t blocks = cap_blocks(B, n_tok, Hq / Hkv, (int)q);
   const ChunkCut c = chunk_cut(blocks, Hkv, max_len);
-  const size_t a = chunk_layout(B, blocks, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.ctas,
-                                c.whole)
-                       .total;
-  if (form == Form::tiles) return a;
-  const size_t b = atoms_workspace_bytes(B, n_tok, Hq, Hkv, d, n, max_q, max_len, total_len);
-  return a > b ? a : b;
+  return chunk_layout(B, blocks, Hkv, d, chunk_cap_tiles(B, max_len, total_len), c.ctas, c.whole)
+      .total;
 }
 
 template <int D>
@@ -1265,11 +1263,7 @@ sdk_status launch_chunk_attn(ChunkParams p, int64_t total_len, char* workspace,
   const Form form =
       pick_form(p.B, p.n_tok, p.Hq, p.Hkv, p.d, p.n, p.max_q, p.max_len, total_len);
   if (form == Form::direct) return launch_chunk_direct(p, total_len, workspace, stream);
-  if (form == Form::atoms) {
-    bool taken = false;
-    const sdk_status s = launch_chunk_atoms(p, total_len, workspace, stream, &taken);
-    if (taken) return s;
-  }
+  if (form == Form::atoms) return launch_chunk_atoms(p, total_len, workspace, stream);
   const int64_t blocks = cap_blocks(p.B, p.n_tok, p.g, p.max_q);
   p.cap_work = blocks;
   const ChunkCut c = chunk_cut(blocks, p.Hkv, p.max_len);

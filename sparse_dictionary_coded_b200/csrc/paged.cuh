@@ -91,7 +91,7 @@ constexpr int64_t kAtomsMaxLen = 1 << 24, kAtomsMaxPairs = 1 << 21, kAtomsMaxWor
 size_t atoms_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int n, int max_q,
                              int max_len, int64_t total_len);
 sdk_status launch_chunk_atoms(ChunkParams p, int64_t total_len, char* workspace,
-                              cudaStream_t stream, bool* taken);
+                              cudaStream_t stream);
 bool direct_fits(int B, int64_t n_tok, int g, int max_q, int max_len);
 size_t direct_workspace_bytes(int B, int64_t n_tok, int Hq, int Hkv, int d, int max_q, int max_len,
                               int64_t total_len);

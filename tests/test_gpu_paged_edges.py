@@ -242,3 +242,16 @@ def test_a_refused_request_leaves_the_others():
     want, tol, _, _ = _attend_ref(c.q, c.dk, c.dv, c.pages, c.table, c.lens, c.cu, True, 0,
                                   1 / math.sqrt(128))
     assert ((out[[0, 1, 25]].double() - want[[0, 1, 4]]).abs() <= tol[[0, 1, 4]]).all()
+
+
+# --------------------------------------------------------------------- workspace
+
+def test_workspace_of_long_contexts():
+    """Few rows over long contexts need the form's own buffers (a tenth of an
+    fp16 copy of the context, two tenths under loose bounds), and these do."""
+    f = sdk.sdk_chunk_attn_workspace_bytes
+    fp16 = lambda tokens, Hkv=8, d=128: tokens * Hkv * 2 * d * 2
+    assert f(1, 1, 32, 8, 128, 32768, 1, 262144, 262144) < 0.1 * fp16(262144)
+    assert f(64, 64, 32, 8, 128, 32768, 1, 32768) < 0.2 * fp16(64 * 32768)
+    c = Case([40000, 3000], [1, 1], Hq=8, Hkv=2, n=3000, seed=27)
+    c.check()
