@@ -64,7 +64,8 @@ def build(verbose=False, force=False):
             if res.returncode != 0:
                 raise RuntimeError("nvcc failed: " + " ".join(cmd))
     if force or jobs or not os.path.exists(LIB):
-        cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs]
+        # by its name alone, so that _binding.so finds the one beside it wherever they are
+        cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libsdk.so", "-o", LIB, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
@@ -87,7 +88,7 @@ def build_binding(force=False):
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
            "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            src, "-o", BINDING, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python", LIB, "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cpu", "-ltorch_python", "-L", PKG, "-lsdk", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
