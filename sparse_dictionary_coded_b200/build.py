@@ -2,7 +2,8 @@
 the host's time counts (_binding.so, g++ over torch's headers) in place; no GPU
 needed to compile.
 
-    python -m sparse_dictionary_coded_b200.build
+    python -m sparse_dictionary_coded_b200.build        # -f: all of it again
+    python sparse_dictionary_coded_b200/build.py -c     # the C ABI alone: no torch
 """
 
 import concurrent.futures
@@ -17,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdk.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_OF = os.path.join(BUILD, "binding.of")   # the Python and torch it was built for
 
 SOURCES = ["api.cu", "chunk_atoms.cu", "chunk_attn.cu", "chunk_direct.cu", "decode.cu", "decode_static.cu", "encode_simt.cu", "encode_small.cu",
            "encode_tc.cu", "out_tc.cu", "paged.cu", "qd_tc.cu"]
@@ -43,8 +45,9 @@ def _stale(obj, src):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(verbose=False, force=False):
-    """Compile every source to an object under _build/ and link libsdk.so."""
+def build(verbose=False, force=False, binding=True):
+    """Compile every source to an object under _build/ and link libsdk.so;
+    with `binding` build _binding.so as well."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     jobs = []
@@ -70,17 +73,29 @@ def build(verbose=False, force=False):
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError("link failed")
-    build_binding(force)
+    if binding:
+        build_binding(force)
     return LIB
+
+
+def binding_stale(src, built_for):
+    """Whether _binding.so is missing, older than its source or built for
+    another Python or torch, whose headers it was compiled with."""
+    if _stale(BINDING, src) or not os.path.exists(BINDING_OF):
+        return True
+    with open(BINDING_OF) as f:
+        return f.read() != built_for
 
 
 def build_binding(force=False):
     """Compile and link _binding.so against torch and libsdk.so."""
-    src = os.path.join(CSRC, "binding.cpp")
-    if not (force or _stale(BINDING, src)):
-        return
     import sysconfig
     import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    built_for = "python %s, torch %s at %s\n" % (sys.version, torch.__version__,
+                                                os.path.dirname(torch.__file__))
+    if not (force or binding_stale(src, built_for)):
+        return
     home = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
@@ -93,7 +108,9 @@ def build_binding(force=False):
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("g++ failed: " + " ".join(cmd))
+    with open(BINDING_OF, "w") as f:
+        f.write(built_for)
 
 
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv, force="-f" in sys.argv))
+    print(build(verbose="-v" in sys.argv, force="-f" in sys.argv, binding="-c" not in sys.argv))
