@@ -265,17 +265,14 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
   make_plan<false>(p, TOK == 1 && blockIdx.x == 0, s_tile0, s_block, s_warp);
   int start = (int)blockIdx.x, stride = (int)gridDim.x;
   if (TOK == 1) {
-    if (blockIdx.x == 0 && gridDim.x > 1) {
+    if (blockIdx.x == 0) {
       plan_work(p, s_block, s_warp);
       return;
     }
-    if (gridDim.x > 1) {
-      start = blockIdx.x - 1;
-      stride = gridDim.x - 1;
-    }
+    --start;
+    --stride;
     // from the last CTA on: the first ones have most of the items
     pack_queries<D>(p, s_block, stride - 1 - start, stride);
-    if (gridDim.x == 1) plan_work(p, s_block, s_warp);
   }
 
   constexpr int LPR = D / 8;           // lanes per record
@@ -1234,6 +1231,7 @@ static sdk_status launch_d(const ChunkParams& p, cudaStream_t stream) {
   int64_t prep = (p.n_tok * p.Hq + kPackRows - 1) / kPackRows;
   if (prep > 4 * num_sms()) prep = 4 * num_sms();
   if (steps <= 80 * num_sms() && p.n_tok * p.Hq <= 32768) {
+    // the plan's CTA and, since a tile has several steps, some more
     const int64_t grid = 1 + (steps < 2 * num_sms() - 1 ? steps : 2 * num_sms() - 1);
     rebuild_kernel<D, 1><<<(unsigned)grid, kRebThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SDK_ERR_CUDA;
