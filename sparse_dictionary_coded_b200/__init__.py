@@ -326,6 +326,14 @@ def _load_binding():
     return b
 
 
+def _on_stream(stream, t):
+    """The context of a call given a stream, which has to be one of the
+    device of its tensors (t: the first): they would run on another one."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return torch.cuda.stream(stream)
+
+
 def _shape(t, name, *dims):
     if tuple(t.shape) != dims:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), dims))
@@ -372,7 +380,7 @@ def sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size,
     workspace to learn of it (sdk_check_status); one made here goes with the
     call."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, lens):
             return sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size, max_new,
                                     n_pages, slot_map, cu_new, new_lens, n_free_out, workspace)
     r = (_calls or _load_binding()).block_tables(
@@ -395,7 +403,7 @@ def sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace=None,
     slots are skipped, slots past the pool recorded in the workspace (give one
     to see it).  Returns pages."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, pages):
             return sdk_paged_store(pages, codes_k, codes_v, slot_map, workspace)
     r = (_calls or _load_binding()).paged_store(pages, codes_k, codes_v, slot_map, workspace)
     if r.__class__ is int:
@@ -413,7 +421,7 @@ def sdk_paged_append(pages, xk, xv, dict_k, dict_v, slot_map, workspace=None,
     codes to the slots slot_map int64 [n_tok] of pages.  Returns the
     workspace (its header records what the device found)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, pages):
             return sdk_paged_append(pages, xk, xv, dict_k, dict_v, slot_map, workspace)
     dev = _cuda_contig(pages, "pages", (torch.int32,)).device
     n_pages, Hkv, page_size = _page_shape(pages)
@@ -461,7 +469,7 @@ def sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q,
     its memory held.  Give a workspace to learn of refusals and bad pages
     (sdk_check_status); the record of one made here goes with the call."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, q):
             return sdk_chunk_attn(q, dict_k, dict_v, pages, block_table, lens, cu_q, max_q, max_len,
                                   total_len, causal, window, scale, out, lse, workspace)
     r = (_calls or _load_binding()).chunk_attn(
@@ -502,7 +510,7 @@ class PagedCodeStore:
         what is left.  free_pages and n_free stay where they are, so a plan
         captured in a CUDA graph takes other pages with every replay."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on_stream(stream, self.n_free):
                 return self.plan(lens, n_new, block_table, max_new, workspace)
         r = sdk_block_tables(lens, n_new, self.free_pages, self.n_free, block_table,
                              self.page_size, max_new, n_pages=self.n_pages,
