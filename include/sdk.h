@@ -510,10 +510,11 @@ SDK_API sdk_status sdk_paged_append(const void* xk, const void* xv, int32_t x_dt
  *   total_len  host bound on the sum of lens (0: B * max_len)
  *   window     0 (none), or >= 1 with SDK_CHUNK_CAUSAL
  *   flags      0 or SDK_CHUNK_CAUSAL
- *   out        device, bf16 [n_tok][Hq][head_dim], 16-byte aligned
- *   lse        device, float [n_tok][Hq], or NULL: log sum_t exp(scale
- *              <q_i, K_t>), natural logarithm (to merge with attention over
- *              other tokens)
+ *   out        device, bf16 [n_tok][Hq][head_dim], 16-byte aligned; q itself,
+ *              or memory apart from it (SDK_ERR_INVALID_ARG)
+ *   lse        device, float [n_tok][Hq], or NULL; apart from q and out:
+ *              log sum_t exp(scale <q_i, K_t>), natural logarithm (to merge
+ *              with attention over other tokens)
  *   workspace  device, >= sdk_chunk_attn_workspace_bytes() of the same sizes
  * Limits: B <= SDK_MAX_REQUESTS, Hq % Hkv == 0, head_dim 64 or 128, scale >
  *   0, n_tok * Hq < 2^31, max_len <= 2^30, max_pages * page_size >= max_len,

@@ -551,6 +551,10 @@ sdk_status sdk_chunk_attn(const void* q, int64_t n_tok, int32_t B, int32_t Hq, i
   if (n_tok > 0 && (!q || !out || !aligned(q, 16) || !aligned(out, 16) ||
                     (lse != nullptr && !aligned(lse, 4))))
     return SDK_ERR_INVALID_ARG;
+  const size_t q_bytes = (size_t)n_tok * Hq * head_dim * 2, lse_bytes = (size_t)n_tok * Hq * 4;
+  if ((out != q && overlap(out, q_bytes, q, q_bytes)) ||
+      (lse != nullptr && (overlap(lse, lse_bytes, q, q_bytes) || overlap(lse, lse_bytes, out, q_bytes))))
+    return SDK_ERR_INVALID_ARG;
   const size_t need = chunk_workspace_bytes(B, n_tok, Hq, Hkv, head_dim, n_atoms, max_q, max_len,
                                             total_len);
   if (ws_bytes < need) return SDK_ERR_CAPACITY;

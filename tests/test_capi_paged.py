@@ -108,6 +108,18 @@ def test_chunk_attn_arguments(lib, kw, status):
     assert lib.sdk_chunk_attn(*a.values(), None) == status
 
 
+def test_chunk_attn_overlapping_outputs(lib):
+    """out may be q, and pass on to the next check; not lie across it."""
+    at = lambda x: ctypes.c_void_p(x)
+    base, size = 1 << 32, 7 * 32 * 128 * 2
+    call = lambda **kw: lib.sdk_chunk_attn(*dict(CHUNK, **kw).values(), None)
+    assert call(out=at(base)) == 3
+    assert call(out=at(base + size)) == 3 and call(out=at(base - size)) == 3
+    assert call(out=at(base + size - 16)) == 1 and call(out=at(base - 16)) == 1
+    assert call(lse=at(base + size)) == 3 and call(lse=at(base + size - 4)) == 1
+    assert call(out=at(base), lse=at(base)) == 1
+
+
 def test_workspace_sizes(lib):
     assert lib.sdk_block_tables_workspace_bytes(0) == 0
     assert lib.sdk_block_tables_workspace_bytes(64) >= 256

@@ -255,3 +255,28 @@ def test_workspace_of_long_contexts():
     assert f(64, 64, 32, 8, 128, 32768, 1, 32768) < 0.2 * fp16(64 * 32768)
     c = Case([40000, 3000], [1, 1], Hq=8, Hkv=2, n=3000, seed=27)
     c.check()
+
+
+# ------------------------------------------------------------ outputs in place
+
+@pytest.mark.parametrize("lens,new,kw", [
+    ([300, 40], [3, 1], {}), ([2000] * 3, [4, 1, 2], dict(d=64)), ([700, 300], [129, 300], {}),
+    ([40000, 50], [2, 1], dict(n=32768))], ids=str)
+def test_out_in_place_of_q(lens, new, kw):
+    """out may be q itself, whichever form runs."""
+    c = Case(lens, new, seed=28, **kw)
+    want = c.run()
+    q = c.q.clone()
+    assert c.run(q=q, out=q) is q and torch.equal(q, want)
+
+
+def test_out_may_not_lie_partly_on_q():
+    c = Case([300], [20], seed=28)
+    room = torch.zeros(30, *c.q.shape[1:], dtype=torch.bfloat16, device="cuda")
+    room[:20] = c.q
+    with pytest.raises(sdk.SdkError, match="SDK_ERR_INVALID_ARG"):
+        c.run(q=room[:20], out=room[1:21])
+    lse = room.view(torch.float32)[:20].reshape(-1)[:160].view(20, 8)
+    with pytest.raises(sdk.SdkError, match="SDK_ERR_INVALID_ARG"):
+        c.run(q=room[:20], lse=lse)
+    assert torch.equal(room[:20], c.q)
