@@ -280,3 +280,22 @@ def test_out_may_not_lie_partly_on_q():
     with pytest.raises(sdk.SdkError, match="SDK_ERR_INVALID_ARG"):
         c.run(q=room[:20], lse=lse)
     assert torch.equal(room[:20], c.q)
+
+
+# ------------------------------------------------------ outputs of a plan apart
+
+@pytest.mark.parametrize("given", [(), ("slot_map",), ("cu_new", "n_free_out")])
+@pytest.mark.parametrize("B,max_new", [(1, 1), (3, 7), (5, 8), (64, 1001)])
+def test_outputs_of_a_plan_lie_apart(B, max_new, given):
+    """What is written to one output, from its first to its last byte, does
+    not reach another."""
+    make = dict(slot_map=lambda: torch.empty(max_new, dtype=torch.int64, device="cuda"),
+                cu_new=lambda: _i32([0] * (B + 1)), n_free_out=lambda: _i32([0]))
+    r = sdk.sdk_block_tables(_i32([0] * B), _i32([0] * B), _i32([0]), _i32([1]), _i32([[-1]] * B), 4,
+                             max_new, **{k: make[k]() for k in given})
+    outs = [r.slot_map, r.cu_new, r.new_lens, r.n_free]
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    for i, t in enumerate(outs):
+        t.fill_(i + 100)
+    assert all((t == i + 100).all() for i, t in enumerate(outs))
