@@ -114,8 +114,10 @@ struct QdCfg {
 // streams the dictionary by TMA, warp 1 issues the MMAs (bf16 atoms and
 // queries, both exact, fp32 sums), warps 2-5 store.  A row is scaled by a
 // power of two that puts its largest entry in [1, 2), so fp16 holds
-// <q, d> with 11 significand bits for atoms of norm 1e-4 to 2900.  Bound by
-// the read of D_K and, with many rows, the stores of QD.
+// <q, d> with 11 significand bits for atoms of norm 1e-4 to 2900 (the rebuilt
+// keys of the other forms are rounded as much; in fp32 a pair of rows would not
+// fit the shared memory, and every token's words would be read twice as often).
+// Bound by the read of D_K and, with many rows, the stores of QD.
 template <int D>
 __global__ void __launch_bounds__(192, 1)
     atoms_qd_kernel(const __grid_constant__ CUtensorMap kmap, ChunkParams p) {
@@ -523,10 +525,14 @@ __device__ __forceinline__ float add_clean_weights(const ChunkParams& p, uint32_
 //      segment, weighted as they are; its exact value is summed up on the way,
 //      and the row is redone with that where the estimate was off by more
 //      than two: sums past 2^31 would wrap, small ones would lose bits.
-//   3. The weights are written as two bf16 parts (16 significand bits) in
-//      the layout the product with D_V reads.
-// Bound by the shared memory: random gathers and additions of 32 lanes need
-// 3.5 passes over the banks on average.
+//   3. The weights are written as two bf16 parts in the layout the product
+//      with D_V reads: 16 significand bits, finer than the fixed point.
+// One token for four requests of 32768: 127 us.  No unit is at its limit: the
+// shared memory pipe is two thirds busy (random gathers and additions of 32
+// lanes need 3.5 passes over the banks on average), the DRAM at 55 % of its
+// peak (529 MB for 134 MB of codes: a pair reads the key words, each row of it
+// the value words, and the pairs of a head at different times), and a share
+// that ends one pair and begins another loads, clears and writes twice.
 template <bool FULL>
 __global__ void __launch_bounds__(kTokThreads, 1)
     atoms_token_kernel(const __grid_constant__ ChunkParams p) {

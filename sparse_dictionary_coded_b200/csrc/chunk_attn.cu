@@ -344,15 +344,17 @@ __global__ void __launch_bounds__(kRebThreads, TOK == 1 ? 2 : 4) rebuild_kernel(
 // The maximum m is only raised when a tile exceeds it by 2^8 (O then is
 // rescaled in TMEM, which is rare); P is 2^7 above its nominal range, so it
 // stays below 2^15 and its smallest fp16 step is 2^-31 of the row's largest
-// term: what 2^18 tokens lose by it is below 2^-13.
+// term: N tokens lose less than N 2^-32 of that by it (2^18 tokens 2^-14).
 // A CTA takes a block (256 packed rows of a KV head), a part of one, or an
 // equal share of all blocks' tiles (chunk_cut says which); a block in several
 // parts or shares leaves partial sums that chunk_join_kernel joins.
-// 2048 tokens over 32768, 32 heads: 910 us of 1248, 1170 TFLOP/s; the tensor
-// pipe is busy two thirds of a tile's 3000 cycles, the rest is the chain score
-// - maximum - exponentials - P of a row (1800 cycles) that the other tile's
-// products hide in part.  The card is at its power limit there (1000 W at
-// 1.5 to 1.8 GHz), so that fewer idle cycles bring less than they seem to.
+// 2048 tokens over 32768, 32 heads: 953 us alone, 1120 TFLOP/s (packing and
+// rebuilding before it 16 and 201); the tensor pipe is busy two thirds of a
+// tile's 3000 cycles, the rest is the chain score - maximum - exponentials - P
+// of a row (1800 cycles) that the other tile's products hide in part.  In a
+// loop of such calls the card is at its power limit (1000 W at 1.5 to 1.8 GHz):
+// the first thirty take 1100 us each, later ones 1240, and fewer idle cycles
+// bring less than they seem to.
 // Tried: a second warpgroup for each tile (half a row a thread) is bound by
 // the exponentials at the same time; half of them on the FMA units instead of
 // a quarter is 2 % slower, none 1 %.
@@ -360,7 +362,8 @@ namespace {
 
 constexpr int kAThreads = 384;     // a warpgroup for each row tile, one of MMA and copy warps
 // registers a thread after the split: 256 x 216 + 128 x 72 = 384 x 168, what
-// the block is launched with (a row's 128 scores stay in registers)
+// the block is launched with.  The code is compiled for 168, a row's 128 scores
+// among them, and spills 312 bytes a thread at either head size.
 constexpr int kRegsLaunch = 168, kRegsRows = 216, kRegsRest = 72;
 static_assert(256 * kRegsRows + 128 * kRegsRest == kAThreads * kRegsLaunch, "register split");
 constexpr float kPUp = 7.0f;       // log2 of P's offset

@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t block_sat_scan(uint32_t v, uint32_t* s_warp,
 // rows a thread takes four neighbours.  The page of a slot comes from the free stack when
 // this call assigns it, so no CTA reads an entry another one writes.  Bound
 // by its launch and the chain load - scan - load for a step of single tokens
-// (2.7 us for 4 requests in a graph), for prompts too (64 of up to 16384 tokens:
+// (2.6 us for 4 requests in a graph), for prompts too (64 of up to 16384 tokens:
 // 4.7 us; four rows far apart, a search each: 6.4 us).
 // T threads: 256 for up to 256 requests, else 1024.
 template <int T>
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(T) block_tables_kernel(TableParams p) {
 // Eight lanes copy one (token, KV head): four 16-byte pieces of key words,
 // four of value words, to the 128-byte line of its slot.  Bound by HBM (the
 // words are read once and written once): 16384 tokens of 8 heads, 33.7 MB, 8.2
-// us, 5.3 in a graph.  One piece a thread: of four, all read before the first
+// us, 5.2 in a graph.  One piece a thread: of four, all read before the first
 // was written (10.2 us), of eight 15.8 us.  I: the type that counts the pieces.
 template <typename I>
 __global__ void __launch_bounds__(256) paged_store_kernel(StoreParams p) {
