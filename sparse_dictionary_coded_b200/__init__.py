@@ -383,9 +383,12 @@ def sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size,
         with _on_stream(stream, lens):
             return sdk_block_tables(lens, n_new, free_pages, n_free, block_table, page_size, max_new,
                                     n_pages, slot_map, cu_new, new_lens, n_free_out, workspace)
-    r = (_calls or _load_binding()).block_tables(
-        lens, n_new, free_pages, n_free, block_table, page_size, max_new, n_pages, slot_map, cu_new,
-        new_lens, n_free_out, workspace)
+    return _block_tables(lens, n_new, free_pages, n_free, block_table, page_size, max_new, n_pages,
+                         slot_map, cu_new, new_lens, n_free_out, workspace, False)
+
+
+def _block_tables(*args):
+    r = (_calls or _load_binding()).block_tables(*args)
     if r.__class__ is int:
         raise SdkError(r, "sdk_block_tables")
     return BlockTables._make(r)
@@ -512,11 +515,9 @@ class PagedCodeStore:
         if stream is not None:
             with _on_stream(stream, self.n_free):
                 return self.plan(lens, n_new, block_table, max_new, workspace)
-        r = sdk_block_tables(lens, n_new, self.free_pages, self.n_free, block_table,
-                             self.page_size, max_new, n_pages=self.n_pages,
-                             workspace=self.workspace if workspace is None else workspace)
-        self.n_free.copy_(r.n_free)
-        return r
+        return _block_tables(lens, n_new, self.free_pages, self.n_free, block_table,
+                             self.page_size, max_new, self.n_pages, None, None, None, None,
+                             self.workspace if workspace is None else workspace, True)
 
     def release(self, page_ids):
         """Puts the pages of a finished request (int32 tensor of distinct

@@ -103,7 +103,8 @@ def build_binding(force=False):
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
            "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            src, "-o", BINDING, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python", "-L", PKG, "-lsdk", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cpu", "-ltorch_python", "-L", PKG, "-lsdk", "-L", os.path.join(os.path.dirname(cuda), "lib64"),
+           "-lcudart", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)

@@ -10,6 +10,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -115,10 +116,12 @@ void check_count(Py_ssize_t n, Py_ssize_t want) {
 }
 
 // lens, n_new, free_pages, n_free, block_table, page_size, max_new, n_pages,
-// slot_map, cu_new, new_lens, n_free_out, workspace
+// slot_map, cu_new, new_lens, n_free_out, workspace, and whether n_free itself
+// holds the new count afterwards (a copy: the plan's CTAs read n_free until
+// they end)
 PyObject* block_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  check_count(n, 13);
+  check_count(n, 14);
   Call c(args);
   const at::Tensor& lens = c.tensor(0, "lens", kI32, 1);
   const at::Tensor& n_new = c.tensor(1, "n_new", kI32, 1);
@@ -146,6 +149,10 @@ PyObject* block_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
         (int32_t*)table.data_ptr(), narrow(table.size(1), "max_pages"), max_new,
         (int64_t*)slots.data_ptr(), (int32_t*)cu.data_ptr(), (int32_t*)new_lens.data_ptr(),
         (int32_t*)left.data_ptr(), ws.data_ptr(), (size_t)ws.numel(), c.stream());
+  if (c.status == SDK_OK && args[13] == Py_True &&
+      cudaMemcpyAsync(n_free.data_ptr(), left.data_ptr(), 4, cudaMemcpyDeviceToDevice,
+                      reinterpret_cast<cudaStream_t>(c.stream())) != cudaSuccess)
+    c.status = SDK_ERR_CUDA;
   if (c.status != SDK_OK) return PyLong_FromLong(c.status);
   PyObject* r = PyTuple_New(5);
   Py_INCREF(args[4]);
